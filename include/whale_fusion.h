@@ -76,6 +76,7 @@ typedef enum { WHALE_FP32 = 0, WHALE_BF16 = 1 } whale_dtype;
 /* device error bits (whale_get_device_error) */
 #define WHALE_DEVERR_TIMEOUT 1
 #define WHALE_DEVERR_OFFSETS 2
+#define WHALE_DEVERR_PAGES 4 /* a cached row or page outside the cache (whale_chunk) */
 
 typedef struct {
   int n_layers;       /* stacked fusion layers (>= 1) */
@@ -339,6 +340,135 @@ whale_status whale_fusion_backward(const whale_config* cfg, const void* wukong_t
                                    float* d_tokens, void* d_states, const whale_layer_grads* grads,
                                    const whale_shape_hint* hint, void* workspace, size_t workspace_bytes,
                                    whale_stream_t stream);
+
+/* ---- norm and rotation of queries and keys -------------------------------------------------
+ *
+ * Per head, after the projections and before the attention: RMSNorm over the head's d_head columns with a gain,
+ * and the rotation of its leading rotary_dim columns by the row's position, in one pass:
+ *   n = x / sqrt(mean(x^2) + eps) * gain
+ *   pair i of n's leading columns, (u, v) -> (u cos t - v sin t, u sin t + v cos t),
+ *   t = position * base^(-2 i / rotary_dim);  the other columns stay n.
+ * Rotated queries and keys have scores that depend on the difference of their positions. No counterpart in the
+ * pages: their attention has no positional term; a history that is cached row by row needs one that is
+ * applied to each row once. eps is cfg->eps; cfg->n_heads and the sizes of the other steps are not
+ * read, d_head = d / n_heads. */
+enum { WHALE_ROTATE_HALVES = 0,   /* pair i = columns i and i + rotary_dim / 2 */
+       WHALE_ROTATE_ADJACENT = 1  /* pair i = columns 2 i and 2 i + 1 */ };
+typedef struct {
+  int rotary_dim; /* 0 (no rotation) .. d_head, a multiple of 16 (bf16) or 8 (fp32) */
+  int layout;     /* WHALE_ROTATE_* */
+  double base;    /* > 0; 10000 is usual */
+} whale_rotary;
+
+/* The queries, or the keys, of one call. Rows of x and y are n_heads * d_head numbers of cfg->dtype, ld_*
+ * elements apart (ld_* and the pointers multiples of 16 bytes), so the K half of K|V rows can be given in place.
+ * y may be x itself with the same stride; otherwise they must not overlap. rows = 0: nothing to do, the
+ * pointers are not read. */
+typedef struct {
+  const void* x;
+  void* y;              /* forward only */
+  const float* gain;    /* device [d_head] */
+  const int* positions; /* device int32 [rows], of any sign */
+  long long rows, ld_x, ld_y;
+  int n_heads;          /* heads of these rows, >= 1 (K may have fewer than Q) */
+} whale_head_rows;
+
+/* q, k: host structs (device pointers inside); either may be null. One kernel for both. Sums and angles
+ * are kept in fp32 and fp64 and rounded once, to cfg->dtype. d_head: 32 or 64 in bf16 mode, 8 .. 128 in fp32 mode. */
+whale_status whale_norm_rotate(const whale_config* cfg, const whale_rotary* rotary, const whale_head_rows* q,
+                               const whale_head_rows* k, whale_stream_t stream);
+
+/* Its backward pass: from x (the forward's input) and dy = dLoss/dy, with dn = the pairs of dy turned back,
+ *   d_gain = sum over rows and heads of dn * x * r,   r = 1 / sqrt(mean(x^2) + eps)
+ *   dx     = r * dn * gain - x * r^3 * mean(dn * gain * x)
+ * dy and dx have type grad_dtype (WHALE_FP32, or WHALE_BF16 in bf16 mode); d_gain is fp32. dx and d_gain are
+ * overwritten (dx may be dy itself with the same stride); d_gain of a part with no rows is 0. The sums of d_gain have a
+ * fixed order: repeated calls agree bit for bit. dq (dk) is read where q (k) is given. Workspace: whale_norm_rotate_workspace_size. */
+typedef struct {
+  const void* dy;
+  void* dx;
+  float* d_gain; /* device [d_head] */
+  long long ld_dy, ld_dx;
+} whale_head_grads;
+size_t whale_norm_rotate_workspace_size(const whale_config* cfg, const whale_head_rows* q, const whale_head_rows* k);
+whale_status whale_norm_rotate_backward(const whale_config* cfg, const whale_rotary* rotary, const whale_head_rows* q,
+                                        const whale_head_rows* k, const whale_head_grads* dq,
+                                        const whale_head_grads* dk, int grad_dtype, void* workspace,
+                                        size_t workspace_bytes, whale_stream_t stream);
+
+/* ---- cached histories (bf16 mode, serving) --------------------------------------------------
+ *
+ * A history grows by a few events at a time, and its projected rows do not change, so serving keeps them:
+ * whale_project_kv (and whale_norm_rotate) on the new rows alone, whale_cache_append, then
+ * whale_cache_attention over the whole cached history, where whale_cross_attention would need every
+ * history's K|V rows packed in one slab. A counterpart in the pages is the projection that is shared by a request's
+ * candidates (pith.science verdict, skeptic critique on footnote 1: K/V amortised once per request); the cache
+ * amortises it over requests.
+ *
+ * The cache is a pool of pages of page_size positions, handed to sequences by the caller:
+ *   pages  [n_pages][planes][n_kv_heads][page_size][d_head], planes = K, V (K alone with WHALE_SHARED_KV)
+ *   scales [n_pages][planes][n_kv_heads][page_size], one byte per row and head (WHALE_CACHE_E4M3 only)
+ * WHALE_CACHE_BF16 keeps the projected rows as they are. WHALE_CACHE_E4M3 keeps e4m3 numbers
+ * that stand for number * 2^e, e = scale - 127 the least integer in [-100, 119] with max|row| <= 448 * 2^e (0 for a
+ * row of zeros): the scaling is exact, each number is rounded once (to nearest even), and reads are exact in bf16. NaNs
+ * stay NaNs and do not count for e; infinities become +-448 * 2^119. */
+typedef enum { WHALE_CACHE_BF16 = 0, WHALE_CACHE_E4M3 = 1 } whale_cache_format;
+typedef struct {
+  void* pages;            /* device, 16-byte aligned, whale_cache_pages_size bytes */
+  unsigned char* scales;  /* device, 16-byte aligned, whale_cache_scales_size bytes; null for WHALE_CACHE_BF16 */
+  int n_pages;
+  int page_size;          /* a power of two, 16 .. 1024 */
+  int n_kv_heads;         /* divides cfg->n_heads: query head h reads K|V head h * n_kv_heads / n_heads */
+  int format;             /* whale_cache_format */
+} whale_cache;
+
+/* A batch of sequences and the rows that a call takes from, or gives to, each. Sequence b owns rows
+ * [offsets[b], offsets[b+1]) of the packed tensor (kv, q or a), n_b of them (0 is fine), and lengths[b]
+ * cached positions; row i of its n_b rows is at position lengths[b] - n_b + i (append, read, causal attention). So the
+ * same chunk appends new rows (lengths counts them) and then attends with them; with n_b = lengths[b] it fills
+ * or reads whole histories. page_table[b][j] is the page of positions [j * page_size, (j+1) * page_size).
+ * Sequences may share pages; pages that are written must not be shared within the call.
+ * Checks on the device: a position below 0 or at or past lengths' bound (max_length, table_stride * page_size), or a page outside
+ * [0, n_pages), is in no page. Such rows are not written, read as zeros (attention sees zero keys and values
+ * there; positions past the bound are not seen), and WHALE_DEVERR_PAGES is recorded. Rows of a packed
+ * tensor past offsets[B] are neither read nor written. Cached rows past lengths[b] are never used, whatever they hold. */
+typedef struct {
+  const int* offsets;    /* device int32 [B+1], ascending from 0 */
+  const int* lengths;    /* device int32 [B] */
+  const int* page_table; /* device int32 [B, table_stride] */
+  int table_stride;
+  int B;
+  int max_new;           /* host bound of every n_b */
+  int max_length;        /* host bound of every length */
+  long long total_new;   /* rows of the packed tensor (>= offsets[B]) */
+} whale_chunk;
+
+/* Bytes of cache->pages and cache->scales (0 for invalid or unsupported configurations; scales 0 for bf16). */
+size_t whale_cache_pages_size(const whale_config* cfg, const whale_cache* cache);
+size_t whale_cache_scales_size(const whale_config* cfg, const whale_cache* cache);
+
+/* Write rows kv [total_new, ld_kv] (bf16; the n_kv_heads * d_head columns of K, then those of V unless WHALE_SHARED_KV,
+ * as whale_project_kv leaves them) to the cache, in its format. */
+whale_status whale_cache_append(const whale_config* cfg, const whale_cache* cache, const whale_chunk* chunk,
+                                const void* kv, long long ld_kv, whale_stream_t stream);
+
+/* The inverse: the last n_b cached rows of each sequence into kv [total_new, ld_kv], as bf16. */
+whale_status whale_cache_read(const whale_config* cfg, const whale_cache* cache, const whale_chunk* chunk, void* kv,
+                              long long ld_kv, whale_stream_t stream);
+
+/* Eq. (4) over the cache: for every row i and head of the chunk, a_i = softmax(q_i K^T / sqrt(d_head)) V over its
+ * sequence's cached positions, q and a [total_new, n_heads * d_head] bf16 with row strides ld_q, ld_a. flags: 0, or
+ * WHALE_ATTEND_CAUSAL: a row sees positions up to its own, lengths[b] - n_b + i. A row that sees nothing
+ * (an empty history, a negative position) gives 0. Softmax statistics and sums are fp32. Cached rows
+ * within lengths[b] must be finite (a causal row's weights of later positions are 0, and 0 times an infinity
+ * is a NaN). Workspace: whale_cache_attention_workspace_size bytes, 256-byte aligned; nothing in it needs to be set or kept
+ * between calls. */
+#define WHALE_ATTEND_CAUSAL 1u
+size_t whale_cache_attention_workspace_size(const whale_config* cfg, const whale_cache* cache,
+                                            const whale_chunk* chunk);
+whale_status whale_cache_attention(const whale_config* cfg, const whale_cache* cache, const whale_chunk* chunk,
+                                   const void* q, long long ld_q, void* a, long long ld_a, unsigned flags,
+                                   void* workspace, size_t workspace_bytes, whale_stream_t stream);
 
 /* Failure detection. Every device-side wait of the library's kernels (a pipeline stage on an
  * mbarrier, one CTA pair waiting for another's published results) gives up after a time limit

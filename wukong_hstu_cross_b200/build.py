@@ -23,7 +23,7 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 def sources() -> list:
     csrc = os.path.join(PKG, "csrc")
     hdr = [os.path.join(ROOT, "include", "whale_fusion.h")]
-    return [os.path.join(csrc, f) for f in sorted(os.listdir(csrc)) if f.endswith((".cu", ".cuh"))] + hdr
+    return [os.path.join(csrc, f) for f in sorted(os.listdir(csrc)) if f.endswith((".cu", ".cuh", ".h"))] + hdr
 
 
 def up_to_date() -> bool:

@@ -1,0 +1,136 @@
+// history_cache.cuh — projected K|V rows of growing histories in a paged cache: writing rows (as bf16, or
+// quantised to e4m3 with one power-of-two scale per row and head) and reading them back.
+//
+// Layout. pages [n_pages][planes][kv_heads][page_size][d_head], planes = K, V (K alone with shared K = V);
+// scales [n_pages][planes][kv_heads][page_size], one byte e + 127. Head-major inside a page: the rows
+// that one head's attention streams are contiguous (page_size * d_head numbers, their scales beside one
+// another), so a tile is one copy and an e4m3 row of 32 bytes costs no half-used sectors.
+//
+// Quantisation of a row x (one head's K or V): e = the least integer with max|x| <= 448 * 2^e, kept in
+// [-100, 119] (119: 448 * 2^119 is finite; -100: 2^-109, the least e4m3 number times 2^-100, is a bf16 number),
+// 0 for a row of zeros; stored = e4m3(x * 2^-e), round to nearest even. The scaling is exact, so the
+// stored number has one rounding, does not depend on how the division is done, and number * 2^e is
+// exact in bf16. A NaN stays a NaN (and does not count for e); an infinity becomes +-448 * 2^119.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "chunk_index.h"
+#include "ptx.cuh"
+
+namespace whale {
+
+constexpr unsigned kErrPages = 4u;
+
+__device__ __forceinline__ uint16_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two e4m3 numbers as f16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint16_t v) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(v));
+  return r;
+}
+
+struct RowsArgs {
+  ChunkView c;
+  const __nv_bfloat16* src;  // append: kv [total, ld]
+  __nv_bfloat16* dst;        // read: kv [total, ld]
+  long long ld;
+  uint8_t* pages;
+  uint8_t* scales;
+};
+
+constexpr int kRowsThreads = 256;
+
+// Append: a row's d_head / 8 lanes take its heads one after another, 16 bytes a lane; the amax of a head is
+// log2(lanes) shuffles. HBM-bound: each number is read once and written once.
+template <int DH, bool FP8>
+__global__ void __launch_bounds__(kRowsThreads) cache_append_kernel(const RowsArgs a) {
+  constexpr int LPH = DH / 8, RPW = 32 / LPH;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, li = lane % LPH;
+  const long long row = ((long long)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5)) * RPW + lane / LPH;
+  const int heads = a.c.planes * a.c.kv_heads;
+  const bool mine = a.c.B > 0 && row < a.c.total && row < a.c.offsets[a.c.B];
+  long long at = -1;
+  if (mine) {
+    const int b = chunk_seq(a.c, row);
+    at = cache_row(a.c, b, (long long)a.c.lengths[b] - (a.c.offsets[b + 1] - row));
+    if (at < 0) atomicOr(&g_device_error, kErrPages);
+  }
+  const bool live = at >= 0;
+  if (!__any_sync(0xffffffffu, live)) return;
+  const uint4* src = reinterpret_cast<const uint4*>(a.src + (live ? row : 0) * a.ld) + li;
+  for (int h = 0; h < heads; ++h) {
+    const long long out = at + ((long long)h << a.c.page_shift);
+    const uint4 w = live ? src[h * LPH] : make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (!FP8) {
+      if (live) *reinterpret_cast<uint4*>(a.pages + (out * DH + li * 8) * 2) = w;
+    } else {
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      float f[8], m = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        f[2 * k] = __uint_as_float(u[k] << 16);
+        f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+        m = fmaxf(m, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+      }
+#pragma unroll
+      for (int o = LPH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const int e = scale_exponent(m);
+      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+      uint32_t q[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        q[k] = (uint32_t)e4m3x2(f[4 * k] * inv, f[4 * k + 1] * inv) |
+               ((uint32_t)e4m3x2(f[4 * k + 2] * inv, f[4 * k + 3] * inv) << 16);
+      if (live) {
+        *reinterpret_cast<uint2*>(a.pages + out * DH + li * 8) = make_uint2(q[0], q[1]);
+        if (li == 0) a.scales[out] = (uint8_t)(e + 127);
+      }
+    }
+  }
+}
+
+// Read: the same lanes the other way; rows in no page come back as zeros.
+template <int DH, bool FP8>
+__global__ void __launch_bounds__(kRowsThreads) cache_read_kernel(const RowsArgs a) {
+  constexpr int LPH = DH / 8, RPW = 32 / LPH;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, li = lane % LPH;
+  const long long row = ((long long)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5)) * RPW + lane / LPH;
+  const int heads = a.c.planes * a.c.kv_heads;
+  if (a.c.B <= 0 || row >= a.c.total || row >= a.c.offsets[a.c.B]) return;
+  const int b = chunk_seq(a.c, row);
+  const long long at = cache_row(a.c, b, (long long)a.c.lengths[b] - (a.c.offsets[b + 1] - row));
+  if (at < 0) atomicOr(&g_device_error, kErrPages);
+  uint4* dst = reinterpret_cast<uint4*>(a.dst + row * a.ld) + li;
+  for (int h = 0; h < heads; ++h) {
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (at >= 0) {
+      const long long in = at + ((long long)h << a.c.page_shift);
+      if constexpr (!FP8) {
+        w = *reinterpret_cast<const uint4*>(a.pages + (in * DH + li * 8) * 2);
+      } else {
+        const uint2 q = *reinterpret_cast<const uint2*>(a.pages + in * DH + li * 8);
+        const float sc = __uint_as_float((uint32_t)a.scales[in] << 23);
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t v = e4m3x2_f16x2((uint16_t)((k < 2 ? q.x : q.y) >> (16 * (k & 1))));
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+          o[k] = pack_bf16x2(f.x * sc, f.y * sc);
+        }
+        w = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+    dst[h * LPH] = w;
+  }
+}
+
+}  // namespace whale

@@ -35,9 +35,12 @@
 #include "attention_bwd.cuh"
 #include "attention_bwd_tc.cuh"
 #include "backward.cuh"
+#include "cache_attention.cuh"
 #include "fp32_path.cuh"
 #include "gemm_2sm.cuh"
 #include "gemm_tc.cuh"
+#include "history_cache.cuh"
+#include "norm_rotate.cuh"
 #include "ptx.cuh"
 
 using namespace whale;
@@ -2577,6 +2580,320 @@ whale_status whale_fusion_backward(const whale_config* cfg, const void* tokens, 
     g = dx;
   }
   return WHALE_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------------
+// norm and rotation of queries and keys (norm_rotate.cuh)
+// ------------------------------------------------------------------------------------------
+namespace {
+
+whale_status check_rotary(const Shape& s, const whale_rotary* r) {
+  if (!r || r->rotary_dim < 0 || r->rotary_dim > s.dh || !(r->base > 0.0) || !std::isfinite(r->base) ||
+      (r->layout != WHALE_ROTATE_HALVES && r->layout != WHALE_ROTATE_ADJACENT))
+    return WHALE_ERR_INVALID_ARG;
+  return r->rotary_dim % (s.bf16 ? 16 : 8) ? WHALE_ERR_UNSUPPORTED : WHALE_OK;
+}
+
+// One part's rows, checked; `grad`: the backward's pointers instead of y.
+whale_status head_rows(const Shape& s, const whale_head_rows* h, const whale_head_grads* g, size_t gs, NrPart* p) {
+  *p = NrPart{};
+  p->heads = 1;
+  if (!h || h->rows == 0) return WHALE_OK;
+  const long long width = (long long)h->n_heads * s.dh;
+  if (h->rows < 0 || h->rows >= (1ll << 31) || h->n_heads < 1 || h->n_heads > (1 << 20) || !h->x || !h->gain ||
+      !h->positions || h->ld_x < width || !aligned16(h->x) || h->ld_x * (long long)s.es % 16)
+    return WHALE_ERR_INVALID_ARG;
+  p->x = h->x;
+  p->gain = h->gain;
+  p->pos = h->positions;
+  p->rows = h->rows;
+  p->ldx = h->ld_x;
+  p->heads = h->n_heads;
+  if (!gs) {
+    if (!h->y || h->ld_y < width || !aligned16(h->y) || h->ld_y * (long long)s.es % 16) return WHALE_ERR_INVALID_ARG;
+    p->y = h->y;
+    p->ldy = h->ld_y;
+    return WHALE_OK;
+  }
+  if (!g || !g->dy || !g->dx || g->ld_dy < width || g->ld_dx < width || !aligned16(g->dy) || !aligned16(g->dx) ||
+      g->ld_dy * (long long)gs % 16 || g->ld_dx * (long long)gs % 16)
+    return WHALE_ERR_INVALID_ARG;
+  p->dy = g->dy;
+  p->lddy = g->ld_dy;
+  p->y = g->dx;
+  p->ldy = g->ld_dx;
+  return WHALE_OK;
+}
+
+void nr_turns(const Shape& s, const whale_rotary& r, NrArgs* a) {
+  a->rot = r.rotary_dim;
+  a->eps = s.eps;
+  for (int i = 0; i < r.rotary_dim / 2; ++i)
+    a->turns[i] = std::pow(r.base, -2.0 * i / r.rotary_dim) / 6.283185307179586476925;
+}
+
+inline long long nr_blocks(const Shape& s, long long rows) {
+  return cdiv<long long>(rows, kNrThreads / (s.dh / (s.bf16 ? 8 : 4)));
+}
+// The backward's blocks stay within a few per SM, so that the gains' partial sums are few.
+constexpr long long kNrBwdBlocks = 4 * kNumSM;
+inline void nr_bwd_blocks(const Shape& s, long long rows0, long long rows1, int* b0, int* b1) {
+  const long long n0 = nr_blocks(s, rows0), n1 = nr_blocks(s, rows1);
+  const long long cap = std::min(kNrBwdBlocks, n0 + n1);
+  *b0 = n0 == 0 ? 0 : (int)std::max(1ll, std::min(n0, cap * n0 / (n0 + n1)));
+  *b1 = n1 == 0 ? 0 : (int)std::max(1ll, std::min(n1, cap - *b0));
+}
+
+template <typename T, int DH>
+whale_status launch_norm_rotate(bool adj, const NrArgs& a, unsigned grid, cudaStream_t st) {
+  return adj ? launch_pdl(norm_rotate_kernel<T, DH, true>, dim3(grid), dim3(kNrThreads), 0, st, a)
+             : launch_pdl(norm_rotate_kernel<T, DH, false>, dim3(grid), dim3(kNrThreads), 0, st, a);
+}
+template <typename T, typename GT, int DH>
+whale_status launch_norm_rotate_backward(bool adj, const NrArgs& a, unsigned grid, cudaStream_t st) {
+  return adj ? launch_pdl(norm_rotate_backward_kernel<T, GT, DH, true>, dim3(grid), dim3(kNrThreads), 0, st, a)
+             : launch_pdl(norm_rotate_backward_kernel<T, GT, DH, false>, dim3(grid), dim3(kNrThreads), 0, st, a);
+}
+
+// ------------------------------------------------------------------------------------------
+// cached histories (history_cache.cuh, cache_attention.cuh)
+// ------------------------------------------------------------------------------------------
+whale_status check_cache(const whale_config* cfg, const whale_cache* k, Shape* s) {
+  WCHECK(validate(cfg, s));
+  if (!k || k->n_pages < 0 || k->page_size < 1 || k->n_kv_heads < 1 ||
+      (k->format != WHALE_CACHE_BF16 && k->format != WHALE_CACHE_E4M3) || s->h % k->n_kv_heads)
+    return WHALE_ERR_INVALID_ARG;
+  if (!s->bf16 || (k->page_size & (k->page_size - 1)) || k->page_size < 16 || k->page_size > 1024)
+    return WHALE_ERR_UNSUPPORTED;
+  // the rows of the pool are numbered in 31 bits (tensor-copy coordinates)
+  if ((long long)k->n_pages * (s->shared_kv ? 1 : 2) * k->n_kv_heads >= (1ll << 31) / k->page_size)
+    return WHALE_ERR_UNSUPPORTED;
+  return WHALE_OK;
+}
+inline size_t cache_rows(const Shape& s, const whale_cache& k) {
+  return (size_t)k.n_pages * (s.shared_kv ? 1 : 2) * k.n_kv_heads * k.page_size;
+}
+
+whale_status check_chunk(const whale_chunk* c) {
+  if (!c || c->B < 0 || c->max_new < 0 || c->max_length < 0 || c->total_new < 0 || c->total_new >= (1ll << 31) ||
+      c->table_stride < 0)
+    return WHALE_ERR_INVALID_ARG;
+  return WHALE_OK;
+}
+
+// The buffers that a non-empty call reads; *empty: there is nothing to do.
+whale_status check_buffers(const whale_cache& k, const whale_chunk& c, bool* empty) {
+  *empty = c.B == 0 || c.total_new == 0;
+  if (*empty) return WHALE_OK;
+  if (!c.offsets || !c.lengths || (!c.page_table && c.table_stride > 0)) return WHALE_ERR_INVALID_ARG;
+  if (k.n_pages > 0 && (!k.pages || !aligned16(k.pages))) return WHALE_ERR_INVALID_ARG;
+  if (k.n_pages > 0 && k.format == WHALE_CACHE_E4M3 && (!k.scales || !aligned16(k.scales))) return WHALE_ERR_INVALID_ARG;
+  return WHALE_OK;
+}
+
+ChunkView chunk_view(const Shape& s, const whale_cache& k, const whale_chunk& c) {
+  ChunkView v{};
+  v.offsets = c.offsets;
+  v.lengths = c.lengths;
+  v.table = c.page_table;
+  v.table_stride = c.table_stride;
+  v.B = c.B;
+  while ((1 << v.page_shift) < k.page_size) ++v.page_shift;
+  v.n_pages = k.n_pages;
+  v.planes = s.shared_kv ? 1 : 2;
+  v.kv_heads = k.n_kv_heads;
+  v.total = c.total_new;
+  v.capacity = std::min<long long>(c.max_length, (long long)c.table_stride * k.page_size);
+  return v;
+}
+
+template <int DH, bool FP8>
+whale_status launch_rows(bool append, const RowsArgs& a, cudaStream_t st) {
+  const long long grid = cdiv<long long>(a.c.total, kRowsThreads / (DH / 8));
+  return launch_pdl(append ? cache_append_kernel<DH, FP8> : cache_read_kernel<DH, FP8>, dim3((unsigned)grid),
+                    dim3(kRowsThreads), 0, st, a);
+}
+
+whale_status cache_rows_call(const whale_config* cfg, const whale_cache* cache, const whale_chunk* chunk,
+                             const void* src, void* dst, long long ld, whale_stream_t stream) {
+  Shape s;
+  WCHECK(check_cache(cfg, cache, &s));
+  WCHECK(check_chunk(chunk));
+  bool empty;
+  WCHECK(check_buffers(*cache, *chunk, &empty));
+  if (empty) return WHALE_OK;
+  const void* rows = src ? src : dst;
+  if (!rows || !aligned16(rows) || ld % 8 || ld < (long long)(s.shared_kv ? 1 : 2) * cache->n_kv_heads * s.dh)
+    return WHALE_ERR_INVALID_ARG;
+  RowsArgs a{};
+  a.c = chunk_view(s, *cache, *chunk);
+  a.src = static_cast<const __nv_bfloat16*>(src);
+  a.dst = static_cast<__nv_bfloat16*>(dst);
+  a.ld = ld;
+  a.pages = static_cast<uint8_t*>(cache->pages);
+  a.scales = cache->scales;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const bool fp8 = cache->format == WHALE_CACHE_E4M3;
+  if (s.dh == 32) return fp8 ? launch_rows<32, true>(src, a, st) : launch_rows<32, false>(src, a, st);
+  return fp8 ? launch_rows<64, true>(src, a, st) : launch_rows<64, false>(src, a, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+whale_status whale_norm_rotate(const whale_config* cfg, const whale_rotary* rotary, const whale_head_rows* q,
+                               const whale_head_rows* k, whale_stream_t stream) {
+  NvtxRange range("whale_norm_rotate");
+  Shape s;
+  WCHECK(validate(cfg, &s));
+  WCHECK(check_rotary(s, rotary));
+  NrArgs a{};
+  WCHECK(head_rows(s, q, nullptr, 0, &a.part[0]));
+  WCHECK(head_rows(s, k, nullptr, 0, &a.part[1]));
+  const long long b0 = nr_blocks(s, a.part[0].rows), b1 = nr_blocks(s, a.part[1].rows);
+  if (b0 + b1 == 0) return WHALE_OK;
+  a.blocks0 = (int)b0;
+  nr_turns(s, *rotary, &a);
+  const bool adj = rotary->layout == WHALE_ROTATE_ADJACENT;
+  const unsigned grid = (unsigned)(b0 + b1);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (s.bf16)
+    return s.dh == 32 ? launch_norm_rotate<__nv_bfloat16, 32>(adj, a, grid, st)
+                      : launch_norm_rotate<__nv_bfloat16, 64>(adj, a, grid, st);
+  switch (s.dh) {
+    case 8: return launch_norm_rotate<float, 8>(adj, a, grid, st);
+    case 16: return launch_norm_rotate<float, 16>(adj, a, grid, st);
+    case 32: return launch_norm_rotate<float, 32>(adj, a, grid, st);
+    case 64: return launch_norm_rotate<float, 64>(adj, a, grid, st);
+    default: return launch_norm_rotate<float, 128>(adj, a, grid, st);
+  }
+}
+
+size_t whale_norm_rotate_workspace_size(const whale_config* cfg, const whale_head_rows* q, const whale_head_rows* k) {
+  Shape s;
+  if (validate(cfg, &s) != WHALE_OK || (q && q->rows < 0) || (k && k->rows < 0)) return 0;
+  return align_up((size_t)(kNrBwdBlocks + 2) * s.dh * 4);
+}
+
+whale_status whale_norm_rotate_backward(const whale_config* cfg, const whale_rotary* rotary, const whale_head_rows* q,
+                                        const whale_head_rows* k, const whale_head_grads* dq,
+                                        const whale_head_grads* dk, int grad_dtype, void* ws, size_t ws_bytes,
+                                        whale_stream_t stream) {
+  NvtxRange range("whale_norm_rotate_backward");
+  Shape s;
+  WCHECK(validate(cfg, &s));
+  WCHECK(check_rotary(s, rotary));
+  if (grad_dtype != WHALE_FP32 && grad_dtype != WHALE_BF16) return WHALE_ERR_INVALID_ARG;
+  if (grad_dtype == WHALE_BF16 && !s.bf16) return WHALE_ERR_UNSUPPORTED;
+  const size_t gs = grad_dtype == WHALE_BF16 ? 2 : 4;
+  if ((q && (!dq || !dq->d_gain)) || (k && (!dk || !dk->d_gain))) return WHALE_ERR_INVALID_ARG;
+  NrArgs a{};
+  WCHECK(head_rows(s, q, dq, gs, &a.part[0]));
+  WCHECK(head_rows(s, k, dk, gs, &a.part[1]));
+  if (!q && !k) return WHALE_OK;
+  if (!ws || ws_bytes < whale_norm_rotate_workspace_size(cfg, q, k) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)))
+    return WHALE_ERR_WORKSPACE;
+  int b0, b1;
+  nr_bwd_blocks(s, a.part[0].rows, a.part[1].rows, &b0, &b1);
+  a.blocks0 = b0;
+  a.partial = static_cast<float*>(ws);
+  nr_turns(s, *rotary, &a);
+  const bool adj = rotary->layout == WHALE_ROTATE_ADJACENT;
+  const unsigned grid = (unsigned)(b0 + b1);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (grid > 0) {
+    whale_status r;
+    if (s.bf16 && gs == 2)
+      r = s.dh == 32 ? launch_norm_rotate_backward<__nv_bfloat16, __nv_bfloat16, 32>(adj, a, grid, st)
+                     : launch_norm_rotate_backward<__nv_bfloat16, __nv_bfloat16, 64>(adj, a, grid, st);
+    else if (s.bf16)
+      r = s.dh == 32 ? launch_norm_rotate_backward<__nv_bfloat16, float, 32>(adj, a, grid, st)
+                     : launch_norm_rotate_backward<__nv_bfloat16, float, 64>(adj, a, grid, st);
+    else
+      switch (s.dh) {
+        case 8: r = launch_norm_rotate_backward<float, float, 8>(adj, a, grid, st); break;
+        case 16: r = launch_norm_rotate_backward<float, float, 16>(adj, a, grid, st); break;
+        case 32: r = launch_norm_rotate_backward<float, float, 32>(adj, a, grid, st); break;
+        case 64: r = launch_norm_rotate_backward<float, float, 64>(adj, a, grid, st); break;
+        default: r = launch_norm_rotate_backward<float, float, 128>(adj, a, grid, st);
+      }
+    WCHECK(r);
+  }
+  return launch_pdl(norm_rotate_gain_kernel, dim3(2), dim3(1024), 0, st, (const float*)ws, b0, b0 + b1, s.dh,
+                    q ? dq->d_gain : nullptr, k ? dk->d_gain : nullptr);
+}
+
+size_t whale_cache_pages_size(const whale_config* cfg, const whale_cache* cache) {
+  Shape s;
+  if (check_cache(cfg, cache, &s) != WHALE_OK) return 0;
+  return cache_rows(s, *cache) * s.dh * (cache->format == WHALE_CACHE_E4M3 ? 1 : 2);
+}
+
+size_t whale_cache_scales_size(const whale_config* cfg, const whale_cache* cache) {
+  Shape s;
+  if (check_cache(cfg, cache, &s) != WHALE_OK || cache->format != WHALE_CACHE_E4M3) return 0;
+  return cache_rows(s, *cache);
+}
+
+whale_status whale_cache_append(const whale_config* cfg, const whale_cache* cache, const whale_chunk* chunk,
+                                const void* kv, long long ld_kv, whale_stream_t stream) {
+  NvtxRange range("whale_cache_append");
+  if (!kv && chunk && chunk->B > 0 && chunk->total_new > 0) return WHALE_ERR_INVALID_ARG;
+  return cache_rows_call(cfg, cache, chunk, kv, nullptr, ld_kv, stream);
+}
+
+whale_status whale_cache_read(const whale_config* cfg, const whale_cache* cache, const whale_chunk* chunk, void* kv,
+                              long long ld_kv, whale_stream_t stream) {
+  NvtxRange range("whale_cache_read");
+  return cache_rows_call(cfg, cache, chunk, nullptr, kv, ld_kv, stream);
+}
+
+size_t whale_cache_attention_workspace_size(const whale_config* cfg, const whale_cache* cache,
+                                            const whale_chunk* chunk) {
+  Shape s;
+  if (check_cache(cfg, cache, &s) != WHALE_OK || check_chunk(chunk) != WHALE_OK) return 0;
+  return kAlign;
+}
+
+whale_status whale_cache_attention(const whale_config* cfg, const whale_cache* cache, const whale_chunk* chunk,
+                                   const void* q, long long ld_q, void* a, long long ld_a, unsigned flags, void* ws,
+                                   size_t ws_bytes, whale_stream_t stream) {
+  NvtxRange range("whale_cache_attention");
+  Shape s;
+  WCHECK(check_cache(cfg, cache, &s));
+  WCHECK(check_chunk(chunk));
+  if (flags & ~WHALE_ATTEND_CAUSAL) return WHALE_ERR_INVALID_ARG;
+  bool empty;
+  WCHECK(check_buffers(*cache, *chunk, &empty));
+  if (empty) return WHALE_OK;
+  if (!q || !a || !aligned16(q) || !aligned16(a) || ld_q % 8 || ld_a % 8 || ld_q < s.d || ld_a < s.d)
+    return WHALE_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < whale_cache_attention_workspace_size(cfg, cache, chunk) ||
+      (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)))
+    return WHALE_ERR_WORKSPACE;
+  CacheAttnArgs p{};
+  p.c = chunk_view(s, *cache, *chunk);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.a = static_cast<__nv_bfloat16*>(a);
+  p.ldq = ld_q;
+  p.lda = ld_a;
+  p.pages = static_cast<const uint8_t*>(cache->pages);
+  p.scales = cache->scales;
+  p.heads = s.h;
+  p.group = s.h / cache->n_kv_heads;
+  p.causal = flags & WHALE_ATTEND_CAUSAL ? 1 : 0;
+  p.scale_log2 = scale_log2_of(s);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const dim3 grid((unsigned)cdiv<long long>(chunk->total_new * s.h, 4));
+  const bool fp8 = cache->format == WHALE_CACHE_E4M3;
+  if (s.dh == 32)
+    return launch_pdl(fp8 ? cache_attend_simple_kernel<32, true> : cache_attend_simple_kernel<32, false>, grid,
+                      dim3(128), 0, st, p);
+  return launch_pdl(fp8 ? cache_attend_simple_kernel<64, true> : cache_attend_simple_kernel<64, false>, grid, dim3(128),
+                    0, st, p);
 }
 
 whale_status whale_test_bounded_waits(unsigned long long limit_ns, whale_stream_t stream) {

@@ -10,7 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
-from ctypes import POINTER, c_float, c_int, c_longlong, c_size_t, c_uint, c_void_p
+from ctypes import POINTER, c_double, c_float, c_int, c_longlong, c_size_t, c_uint, c_void_p
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libwhale_fusion.so")
 HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "whale_fusion.h")
@@ -18,7 +18,10 @@ HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))
 WHALE_FP32, WHALE_BF16 = 0, 1
 WHALE_SHARED_KV, WHALE_TIED_GATE, WHALE_DEBUG, WHALE_PREPARED_WEIGHTS = 1, 2, 4, 8
 WHALE_MATERIALIZED_KV = 16
-WHALE_DEVERR_TIMEOUT, WHALE_DEVERR_OFFSETS = 1, 2
+WHALE_DEVERR_TIMEOUT, WHALE_DEVERR_OFFSETS, WHALE_DEVERR_PAGES = 1, 2, 4
+WHALE_ROTATE_HALVES, WHALE_ROTATE_ADJACENT = 0, 1
+WHALE_CACHE_BF16, WHALE_CACHE_E4M3 = 0, 1
+WHALE_ATTEND_CAUSAL = 1
 WHALE_NOALLOC_SCRATCH_BYTES = 32 << 20
 STATUS = {0: "WHALE_OK", 1: "WHALE_ERR_INVALID_ARG", 2: "WHALE_ERR_UNSUPPORTED", 3: "WHALE_ERR_CUDA",
           4: "WHALE_ERR_WORKSPACE", 5: "WHALE_ERR_DEVICE_CHECK"}
@@ -50,6 +53,29 @@ class whale_shape_hint(ctypes.Structure):
 
 class whale_kernel_time(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_char_p), ("ms", c_float)]
+
+
+class whale_rotary(ctypes.Structure):
+    _fields_ = [("rotary_dim", c_int), ("layout", c_int), ("base", c_double)]
+
+
+class whale_head_rows(ctypes.Structure):
+    _fields_ = [("x", c_void_p), ("y", c_void_p), ("gain", c_void_p), ("positions", c_void_p), ("rows", c_longlong),
+                ("ld_x", c_longlong), ("ld_y", c_longlong), ("n_heads", c_int)]
+
+
+class whale_head_grads(ctypes.Structure):
+    _fields_ = [("dy", c_void_p), ("dx", c_void_p), ("d_gain", c_void_p), ("ld_dy", c_longlong), ("ld_dx", c_longlong)]
+
+
+class whale_cache(ctypes.Structure):
+    _fields_ = [("pages", c_void_p), ("scales", c_void_p), ("n_pages", c_int), ("page_size", c_int),
+                ("n_kv_heads", c_int), ("format", c_int)]
+
+
+class whale_chunk(ctypes.Structure):
+    _fields_ = [("offsets", c_void_p), ("lengths", c_void_p), ("page_table", c_void_p), ("table_stride", c_int),
+                ("B", c_int), ("max_new", c_int), ("max_length", c_int), ("total_new", c_longlong)]
 
 
 class WhaleError(RuntimeError):
@@ -94,6 +120,22 @@ _SIGS = {
                                      POINTER(whale_layer_grads), POINTER(whale_shape_hint), _P, c_size_t, _P], c_int),
     "whale_fusion_backward": ([POINTER(whale_config), _P, _P, _P, POINTER(whale_layer_weights), _P, _P, _P,
                                POINTER(whale_layer_grads), POINTER(whale_shape_hint), _P, c_size_t, _P], c_int),
+    "whale_norm_rotate": ([POINTER(whale_config), POINTER(whale_rotary), POINTER(whale_head_rows),
+                           POINTER(whale_head_rows), _P], c_int),
+    "whale_norm_rotate_workspace_size": ([POINTER(whale_config), POINTER(whale_head_rows), POINTER(whale_head_rows)],
+                                         c_size_t),
+    "whale_norm_rotate_backward": ([POINTER(whale_config), POINTER(whale_rotary), POINTER(whale_head_rows),
+                                    POINTER(whale_head_rows), POINTER(whale_head_grads), POINTER(whale_head_grads),
+                                    c_int, _P, c_size_t, _P], c_int),
+    "whale_cache_pages_size": ([POINTER(whale_config), POINTER(whale_cache)], c_size_t),
+    "whale_cache_scales_size": ([POINTER(whale_config), POINTER(whale_cache)], c_size_t),
+    "whale_cache_append": ([POINTER(whale_config), POINTER(whale_cache), POINTER(whale_chunk), _P, c_longlong, _P],
+                           c_int),
+    "whale_cache_read": ([POINTER(whale_config), POINTER(whale_cache), POINTER(whale_chunk), _P, c_longlong, _P], c_int),
+    "whale_cache_attention_workspace_size": ([POINTER(whale_config), POINTER(whale_cache), POINTER(whale_chunk)],
+                                             c_size_t),
+    "whale_cache_attention": ([POINTER(whale_config), POINTER(whale_cache), POINTER(whale_chunk), _P, c_longlong, _P,
+                               c_longlong, c_uint, _P, c_size_t, _P], c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -359,3 +401,209 @@ def whale_get_device_error(stream=None) -> int:
     if st not in (0, 5):
         _check(st, "whale_get_device_error")
     return code.value
+
+
+# ------------------------------------------------------------------------------------------------
+# norm and rotation, cached histories: descriptors (each keeps its tensors alive) and entry points
+# ------------------------------------------------------------------------------------------------
+def _rows_of(name, t, dtypes, ndim=2):
+    """Checks a tensor that the library reads as rows: innermost stride 1, on the current device. Returns it."""
+    import torch
+    if t.dtype not in dtypes or t.dim() != ndim:
+        raise ValueError(f"{name}: {ndim} dimensions of {' or '.join(map(str, dtypes))} expected, got {t.dim()} of {t.dtype}")
+    if t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
+    return t
+
+
+def _ld(t) -> int:
+    return int(t.stride(0)) if t.shape[0] > 1 and t.shape[1] > 0 else int(t.shape[1])
+
+
+def _ints(name, t, n=None):
+    import torch
+    _rows_of(name, t, (torch.int32,), 1)
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name}: {n} entries expected, got {t.numel()}")
+    return t
+
+
+def make_rotary(rotary_dim, base=10000.0, layout=WHALE_ROTATE_HALVES) -> whale_rotary:
+    return whale_rotary(int(rotary_dim), int(layout), float(base))
+
+
+def head_rows(x, gain, positions, y=None) -> whale_head_rows:
+    """The queries (or keys) of one norm-and-rotation call: x and y [rows, n_heads * d_head] (any row
+    stride), gain fp32 [d_head], positions int32 [rows]. y is the forward's output (x itself: in place)."""
+    import torch
+    _rows_of("x", x, (torch.bfloat16, torch.float32))
+    _rows_of("gain", gain, (torch.float32,), 1)
+    _ints("positions", positions, x.shape[0])
+    if x.shape[1] < gain.numel() or gain.numel() == 0 or x.shape[1] % gain.numel():
+        raise ValueError(f"x: {x.shape[1]} columns are no whole number of heads of {gain.numel()}")
+    if y is not None:
+        _rows_of("y", y, (x.dtype,))
+        if y.shape != x.shape:
+            raise ValueError(f"y: {tuple(y.shape)} for x {tuple(x.shape)}")
+    r = whale_head_rows(_ptr(x), _ptr(y), _ptr(gain), _ptr(positions), x.shape[0], _ld(x), 0 if y is None else _ld(y),
+                        x.shape[1] // gain.numel())
+    r._keepalive = (x, gain, positions, y)
+    return r
+
+
+def head_grads(dy, dx, d_gain) -> whale_head_grads:
+    """The gradients of one part: dy and dx [rows, n_heads * d_head] of the call's grad_dtype, d_gain fp32 [d_head]."""
+    import torch
+    _rows_of("dy", dy, (torch.bfloat16, torch.float32))
+    _rows_of("dx", dx, (dy.dtype,))
+    _rows_of("d_gain", d_gain, (torch.float32,), 1)
+    if dx.shape != dy.shape:
+        raise ValueError(f"dx: {tuple(dx.shape)} for dy {tuple(dy.shape)}")
+    r = whale_head_grads(_ptr(dy), _ptr(dx), _ptr(d_gain), _ld(dy), _ld(dx))
+    r._keepalive = (dy, dx, d_gain)
+    return r
+
+
+def _types(cfg, rows, grads=None, grad_dtype=None):
+    """Rows and gradients agree with the call's types and with each other (the C ABI cannot see a tensor's type)."""
+    import torch
+    for r, g in zip(rows, grads or (None,) * len(rows)):
+        if r is None or not hasattr(r, "_keepalive"):
+            continue
+        x, gain = r._keepalive[:2]
+        if x.dtype != (torch.bfloat16 if cfg.dtype == WHALE_BF16 else torch.float32):
+            raise ValueError(f"rows of {x.dtype} for this configuration's type")
+        if gain.numel() * cfg.n_heads != cfg.d:
+            raise ValueError(f"gain: {gain.numel()} entries for d_head {cfg.d // max(cfg.n_heads, 1)}")
+        if g is not None and hasattr(g, "_keepalive"):
+            dy, _, dg = g._keepalive
+            if dy.dtype != (torch.bfloat16 if grad_dtype == WHALE_BF16 else torch.float32) or dy.shape != x.shape \
+                    or dg.numel() != gain.numel():
+                raise ValueError(f"gradients {tuple(dy.shape)} of {dy.dtype} for rows {tuple(x.shape)}")
+
+
+def _ref(s):
+    return None if s is None else ctypes.byref(s)
+
+
+def whale_norm_rotate(cfg, rotary, q, k, stream=None, raw=False):
+    """Per-head RMS norm and rotation by position (see include/whale_fusion.h); q, k: head_rows or None."""
+    _types(cfg, (q, k))
+    st = _lib.whale_norm_rotate(ctypes.byref(cfg), ctypes.byref(rotary), _ref(q), _ref(k), _stream(stream))
+    if raw:
+        return st
+    _check(st, "whale_norm_rotate")
+
+
+def whale_norm_rotate_workspace_size(cfg, q, k) -> int:
+    return int(_lib.whale_norm_rotate_workspace_size(ctypes.byref(cfg), _ref(q), _ref(k)))
+
+
+def whale_norm_rotate_backward(cfg, rotary, q, k, dq, dk, grad_dtype, workspace, workspace_bytes=None, stream=None,
+                               raw=False):
+    _types(cfg, (q, k), (dq, dk), grad_dtype)
+    st = _lib.whale_norm_rotate_backward(ctypes.byref(cfg), ctypes.byref(rotary), _ref(q), _ref(k), _ref(dq), _ref(dk),
+                                         int(grad_dtype), _ptr(workspace), _ws_bytes(workspace, workspace_bytes),
+                                         _stream(stream))
+    if raw:
+        return st
+    _check(st, "whale_norm_rotate_backward")
+
+
+def make_cache(pages, scales=None) -> whale_cache:
+    """A cache over pages [n_pages, planes, n_kv_heads, page_size, d_head] (bf16, or e4m3 as uint8 or
+    float8_e4m3fn with scales uint8 [n_pages, planes, n_kv_heads, page_size]); both contiguous."""
+    import torch
+    e4m3 = scales is not None
+    _rows_of("pages", pages, (torch.uint8, torch.float8_e4m3fn) if e4m3 else (torch.bfloat16,), 5)
+    if e4m3:
+        _rows_of("scales", scales, (torch.uint8,), 4)
+        if scales.shape != pages.shape[:4]:
+            raise ValueError(f"scales: {tuple(scales.shape)} for pages {tuple(pages.shape)}")
+    if not pages.is_contiguous() or (e4m3 and not scales.is_contiguous()):
+        raise ValueError("pages and scales must be contiguous")
+    k = whale_cache(_ptr(pages), _ptr(scales), pages.shape[0], pages.shape[3], pages.shape[2],
+                    WHALE_CACHE_E4M3 if e4m3 else WHALE_CACHE_BF16)
+    k._keepalive = (pages, scales)
+    return k
+
+
+def make_chunk(offsets, lengths, page_table, max_new, max_length, total_new) -> whale_chunk:
+    """A batch of sequences (see whale_chunk): offsets int32 [B+1], lengths int32 [B], page_table int32
+    [B, table_stride], and the host's bounds of rows per sequence, of lengths, and of rows in all."""
+    import torch
+    _ints("lengths", lengths)
+    _ints("offsets", offsets, lengths.numel() + 1)
+    _rows_of("page_table", page_table, (torch.int32,))
+    if page_table.shape[0] != lengths.numel():
+        raise ValueError(f"page_table: {page_table.shape[0]} sequences, lengths has {lengths.numel()}")
+    if not page_table.is_contiguous():
+        raise ValueError("page_table must be contiguous")
+    c = whale_chunk(_ptr(offsets), _ptr(lengths), _ptr(page_table), page_table.shape[1], lengths.numel(), int(max_new),
+                    int(max_length), int(total_new))
+    c._keepalive = (offsets, lengths, page_table)
+    return c
+
+
+def _packed(name, t, cfg, cache, chunk, width):
+    """A packed [total_new, width] bf16 tensor's row stride, and the cache's planes and d_head, checked."""
+    import torch
+    if isinstance(t, int) or t is None:
+        return width
+    _rows_of(name, t, (torch.bfloat16,))
+    if t.shape[0] < chunk.total_new or t.shape[1] != width:
+        raise ValueError(f"{name}: {tuple(t.shape)}, [{chunk.total_new}, {width}] expected")
+    pages = getattr(cache, "_keepalive", (None,))[0]
+    if pages is not None and (pages.shape[4] * cfg.n_heads != cfg.d
+                              or pages.shape[1] != (1 if cfg.flags & WHALE_SHARED_KV else 2)):
+        raise ValueError(f"pages {tuple(pages.shape)} do not fit the configuration")
+    return _ld(t)
+
+
+def _kv_width(cfg, cache):
+    return (1 if cfg.flags & WHALE_SHARED_KV else 2) * cache.n_kv_heads * (cfg.d // max(cfg.n_heads, 1))
+
+
+def whale_cache_pages_size(cfg, cache) -> int:
+    return int(_lib.whale_cache_pages_size(ctypes.byref(cfg), ctypes.byref(cache)))
+
+
+def whale_cache_scales_size(cfg, cache) -> int:
+    return int(_lib.whale_cache_scales_size(ctypes.byref(cfg), ctypes.byref(cache)))
+
+
+def whale_cache_append(cfg, cache, chunk, kv, stream=None, raw=False):
+    """Write the chunk's K|V rows to the cache, in its format."""
+    ld = _packed("kv", kv, cfg, cache, chunk, _kv_width(cfg, cache))
+    st = _lib.whale_cache_append(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk), _ptr(kv), ld,
+                                 _stream(stream))
+    if raw:
+        return st
+    _check(st, "whale_cache_append")
+
+
+def whale_cache_read(cfg, cache, chunk, kv, stream=None, raw=False):
+    """Read the chunk's K|V rows back from the cache, as bf16."""
+    ld = _packed("kv", kv, cfg, cache, chunk, _kv_width(cfg, cache))
+    st = _lib.whale_cache_read(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk), _ptr(kv), ld,
+                               _stream(stream))
+    if raw:
+        return st
+    _check(st, "whale_cache_read")
+
+
+def whale_cache_attention_workspace_size(cfg, cache, chunk) -> int:
+    return int(_lib.whale_cache_attention_workspace_size(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk)))
+
+
+def whale_cache_attention(cfg, cache, chunk, q, a, workspace, workspace_bytes=None, flags=0, stream=None, raw=False):
+    """Attention of the chunk's rows q over the cached histories (flags: WHALE_ATTEND_CAUSAL) into a."""
+    ldq, lda = _packed("q", q, cfg, cache, chunk, cfg.d), _packed("a", a, cfg, cache, chunk, cfg.d)
+    st = _lib.whale_cache_attention(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk), _ptr(q), ldq, _ptr(a),
+                                    lda, int(flags), _ptr(workspace), _ws_bytes(workspace, workspace_bytes),
+                                    _stream(stream))
+    if raw:
+        return st
+    _check(st, "whale_cache_attention")
