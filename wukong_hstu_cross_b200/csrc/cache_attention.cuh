@@ -1,9 +1,33 @@
-// cache_attention.cuh — attention of a chunk of rows over the paged cache:
+// cache_attention.cuh — attention of a chunk of rows over the paged cache, few rows per sequence (a new event,
+// a request's tokens):
 //   a_i = sum_j p_ij v_j,  p_i = softmax_j(q_i . k_j / sqrt(d_head)) over the sequence's cached positions j
 //   (causal: j <= position of row i; a row that sees nothing gives 0).
-// Query head h reads K|V head h * kv_heads / n_heads.
+// Query head h reads K|V head h * kv_heads / n_heads, so the n_b * group rows (token, head of the group) of one
+// sequence and K|V head share every cached row: row r is token r / group, head kvh * group + r % group.
+//
+// Bound: HBM (each cached row is read once; 2 * n_b * group operations per byte of bf16).
+//
+// Split. Units of kCaTile positions of one (sequence, K|V head, block of BM rows) are laid end to end, and warp w of
+// W takes the contiguous slice [w T / W, (w + 1) T / W): every warp streams the same number of bytes whatever the
+// lengths. A warp works alone (its own ring of shared memory, no block barrier after the prologue), keeps (m, l, o)
+// of its BM rows in registers, and leaves a partial in the workspace where its slice cuts an item: at most two a
+// warp. cache_attend_merge_kernel joins them in the order of the warps, so results do not depend on timing.
+//
+// The stream: cp.async, STAGES - 1 tiles ahead; the lanes look up the page of one position each, a tile earlier still.
+// Rows past the end and rows in no page are zero-filled, so what unwritten rows hold is never used.
+//
+// Products: warp-level m16n8k16 with fp32 sums. bf16 cache: K and V by ldmatrix. e4m3 cache: the
+// fragments are converted from the bytes in registers, to f16 (every e4m3 number is an f16 number); a lane's bytes of a K
+// row are contiguous (the order of d_head inside a product is free as long as q has the same), and the
+// positions of a tile are numbered so that a lane's scores are 8 neighbouring ones, whose scales it
+// reads as one word. K's scale multiplies the score, V's the weight. Queries are brought into f16's range by a
+// power of two of each row (exact down to 2^-39 of the row's largest), weights are 2^(s - m + 7 + e - E), E the largest V
+// exponent so far: 11 significant bits down to 2^-21 of the largest, where bf16 weights have 8.
 #pragma once
 
+#include <cuda_fp16.h>
+
+#include "attention_bwd.cuh"
 #include "history_cache.cuh"
 
 namespace whale {
@@ -16,70 +40,602 @@ struct CacheAttnArgs {
   const uint8_t* pages;
   const uint8_t* scales;
   int heads, group, causal;
-  float scale_log2;  // log2(e) / sqrt(d_head)
+  int max_new;             // rows of a sequence, at most
+  int n_qb;                // row blocks of a sequence, at most
+  float scale_log2;        // log2(e) / sqrt(d_head)
+  float* part_o;           // [2 W, BM, DH]
+  float* part_ml;          // [2 W, BM, 2]
+  long long* before;       // [B + 1] units before each sequence, and their number
 };
 
-// One warp per (row, head): a lane takes every 32nd position with a running maximum, sum and output of its
-// own (fp32); the lanes meet by shuffles at the end.
+constexpr int kCaTile = 32;     // positions of a unit
+constexpr int kCaWarps = 8;     // warps of a CTA (one CTA per SM)
+constexpr int kCaThreads = 32 * kCaWarps;
+constexpr int kCaMinUnits = 4;  // a warp's least share, where there is little work: partials cost more than units
+constexpr float kCaLazy = 8.0f; // log2 headroom before the reference is raised
+
 template <int DH, bool FP8>
-__global__ void __launch_bounds__(128) cache_attend_simple_kernel(const CacheAttnArgs p) {
+struct CaTile {
+  static constexpr int ROW = FP8 ? DH : 2 * DH;           // bytes of a row
+  static constexpr int PLANE = kCaTile * ROW;
+  static constexpr int SCALES = FP8 ? 2 * kCaTile : 0;    // K's, V's
+  static constexpr int BYTES = 2 * PLANE + SCALES;
+  static constexpr int STAGES = 24576 / BYTES < 8 ? 24576 / BYTES : 8;
+  static constexpr int SMEM = kCaWarps * STAGES * BYTES;
+  static_assert(STAGES >= 3 && BYTES % 16 == 0 && SMEM <= 220 * 1024, "ring");
+  // byte offset of 16-byte chunk `ch` of row r: conflict-free for the fragment reads below
+  static __device__ __forceinline__ int at(int r, int ch) {
+    if constexpr (!FP8) return r * ROW + ((ch ^ (DH == 64 ? r & 7 : (r >> 1) & 3)) << 4);
+    // one line of 128 bytes holds the rows that lanes t = 0..3 read together (8 positions apart): give each its quarter
+    else if constexpr (DH == 64) return (r ^ ((r >> 4) & 1)) * ROW + ((ch ^ ((r >> 2) & 2)) << 4);
+    else return (r ^ (((r >> 2) & 2) | ((r >> 4) & 1))) * ROW + (ch << 4);
+  }
+};
+
+// Units of sequence b per (K|V head, row block), its rows and positions.
+struct CaSeq {
+  int first_row, rows, take; // rows of the packed tensor; of them within max_new
+  int len;                  // positions, within the cache's bounds
+  int units, blocks;        // tiles (1 for an empty history: its rows are written as zeros), row blocks
+};
+__device__ __forceinline__ CaSeq ca_seq(const CacheAttnArgs& p, int b, int bm) {
+  CaSeq s;
+  s.first_row = chunk_off(p.c, b);
+  s.rows = chunk_off(p.c, b + 1) - s.first_row;
+  s.take = min(s.rows, p.max_new);
+  const long long n = p.c.lengths[b];
+  s.len = (int)(n < 0 ? 0 : (n > p.c.capacity ? p.c.capacity : n));
+  s.units = s.len <= kCaTile ? 1 : (s.len + kCaTile - 1) / kCaTile;
+  s.blocks = s.take <= 0 ? 0 : (s.take * p.group + bm - 1) / bm;
+  return s;
+}
+__device__ __forceinline__ long long ca_units(const CacheAttnArgs& p, int b, int bm) {
+  const CaSeq s = ca_seq(p, b, bm);
+  return (long long)s.units * s.blocks * p.c.kv_heads;
+}
+__device__ __forceinline__ long long ca_workers(long long T, long long W) {
+  const long long w = (T + kCaMinUnits - 1) / kCaMinUnits;
+  return w < W ? w : W;
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+
+template <int DH, bool FP8, int MT>
+__global__ void __launch_bounds__(kCaThreads, 1) cache_attend_kernel(const CacheAttnArgs p) {
+  using L = CaTile<DH, FP8>;
+  constexpr int BM = 16 * MT, NT = kCaTile / 8, KS = DH / 16, ND = DH / 8, STAGES = L::STAGES;
+  extern __shared__ __align__(128) uint8_t ring_all[];
+  __shared__ long long sums[kCaThreads + 1];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const long long item = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const long long row = item / p.heads;
-  const int h = (int)(item % p.heads), kvh = h / p.group;
-  if (row >= p.c.total || row >= p.c.offsets[p.c.B]) return;
-  const int b = chunk_seq(p.c, row);
-  const long long len = min((long long)p.c.lengths[b], p.c.capacity);
-  const long long pos = p.c.lengths[b] - (p.c.offsets[b + 1] - row);
-  if (p.c.lengths[b] > len && lane == 0) atomicOr(&g_device_error, kErrPages);
-  const long long end = p.causal ? min(len, pos + 1) : len;
-  float q[DH], o[DH], m = -INFINITY, l = 0.f;
+
+  // units before each thread's run of sequences
+  const int run = (p.c.B + kCaThreads - 1) / kCaThreads;
+  const int b_lo = min(p.c.B, tid * run), b_hi = min(p.c.B, b_lo + run);
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += ca_units(p, b, BM);
+  long long scan = mine;
 #pragma unroll
-  for (int k = 0; k < DH; ++k) {
-    q[k] = __bfloat162float(p.q[row * p.ldq + h * DH + k]) * p.scale_log2;
-    o[k] = 0.f;
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += v;
   }
-  for (long long j = lane; j < end; j += 32) {
-    const long long at = cache_row(p.c, b, j);
-    if (at < 0) atomicOr(&g_device_error, kErrPages);
-    float kv[2][DH];
+  if (lane == 31) sums[warp] = scan;
+  __syncthreads();
+  long long base = 0;
+  for (int w = 0; w < warp; ++w) base += sums[w];
+  __syncthreads();
+  sums[tid + 1] = base + scan;
+  if (tid == 0) sums[0] = 0;
+  if (blockIdx.x == 0) {  // for the merge
+    long long at = base + scan - mine;
+    for (int b = b_lo; b < b_hi; ++b) {
+      p.before[b] = at;
+      at += ca_units(p, b, BM);
+    }
+    if (tid == kCaThreads - 1) p.before[p.c.B] = base + scan;
+  }
+  __syncthreads();
+  const long long T = sums[kCaThreads];
+  const long long W = ca_workers(T, (long long)gridDim.x * kCaWarps);
+  const long long gw = (long long)warp * gridDim.x + blockIdx.x;  // neighbours on different SMs
+  if (gw >= W) return;
+  const long long u_lo = gw * T / W, u_hi = (gw + 1) * T / W;
+  if (u_lo >= u_hi) return;
+
+  // the sequence of the first unit
+  int b, lo = 0, hi = kCaThreads - 1;
+  while (lo < hi) {  // largest run that starts at or before u_lo and is not empty behind it
+    const int mid = (lo + hi + 1) >> 1;
+    if (sums[mid] <= u_lo) lo = mid;
+    else hi = mid - 1;
+  }
+  b = min(p.c.B, lo * run);
+  long long at = sums[lo];
+  for (;;) {
+    const long long n = ca_units(p, b, BM);
+    if (at + n > u_lo || b + 1 >= p.c.B) break;
+    at += n;
+    ++b;
+  }
+
+  const uint32_t ring = smem_u32(ring_all) + warp * (STAGES * L::BYTES);
+  const uint8_t* const pages = p.pages;
+  long long u = u_lo;
+  while (u < u_hi) {
+    const CaSeq s = ca_seq(p, b, BM);
+    const long long n_b = (long long)s.units * s.blocks * p.c.kv_heads;
+    if (u >= at + n_b) {
+      if (b + 1 >= p.c.B) return;
+      at += n_b;
+      ++b;
+      continue;
+    }
+    const int item = (int)((u - at) / s.units), t_lo = (int)((u - at) - (long long)item * s.units);
+    const int t_hi = (int)min((long long)s.units, t_lo + (u_hi - u));
+    const int kvh = item / s.blocks, r0 = (item - kvh * s.blocks) * BM;
+    const int n_rows = min(BM, s.take * p.group - r0);
+    const long long pos0 = (long long)p.c.lengths[b] - s.rows;  // position of the sequence's first row
+    if (lane == 0 && p.c.lengths[b] > s.len) atomicOr(&g_device_error, kErrPages);
+    if (lane == 0 && s.rows > s.take) atomicOr(&g_device_error, kErrOffsets);
+
+    // queries as A fragments, ends of the rows
+    uint32_t qf[MT][KS][4];
+    int end[MT][2];
+    float fac[MT][2];  // log2(e) / sqrt(d_head), and for e4m3 the power of two taken out of the row
+    int end_min = s.len;
 #pragma unroll
-    for (int pl = 0; pl < 2; ++pl) {
-      const long long r = at + ((long long)((p.c.planes == 2 ? pl : 0) * p.c.kv_heads + kvh) << p.c.page_shift);
-      const float sc = FP8 && at >= 0 ? __uint_as_float((uint32_t)p.scales[r] << 23) : 1.f;
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int k = 0; k < DH; ++k) {
-        if (at < 0) kv[pl][k] = 0.f;
-        else if constexpr (FP8) {
-          __half_raw hr = __nv_cvt_fp8_to_halfraw(p.pages[r * DH + k], __NV_E4M3);
-          kv[pl][k] = __half2float(*reinterpret_cast<__half*>(&hr)) * sc;
-        } else kv[pl][k] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.pages)[r * DH + k]);
+      for (int hh = 0; hh < 2; ++hh) {
+        const int r = 16 * m + 8 * hh + g;
+        const bool live = r < n_rows;
+        const int tok = live ? (r0 + r) / p.group : 0;
+        const int head = kvh * p.group + (live ? (r0 + r) % p.group : 0);
+        const __nv_bfloat16* src = p.q + (long long)(s.first_row + tok) * p.ldq + head * DH;
+        fac[m][hh] = p.scale_log2;
+        const long long e = p.causal ? min((long long)s.len, pos0 + tok + 1) : (long long)s.len;
+        end[m][hh] = live ? (int)max(e, 0ll) : 0;
+        if (live) end_min = min(end_min, end[m][hh]);
+        if constexpr (!FP8) {
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            qf[m][k][hh] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * t) : 0u;
+            qf[m][k][2 + hh] = live ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 2 * t + 8) : 0u;
+          }
+        } else {
+          uint32_t w[2 * KS];
+          float f[4 * KS], mx = 0.f;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const uint2 v = live ? *reinterpret_cast<const uint2*>(src + t * (DH / 4) + 4 * k) : make_uint2(0u, 0u);
+            w[2 * k] = v.x;
+            w[2 * k + 1] = v.y;
+          }
+#pragma unroll
+          for (int k = 0; k < 2 * KS; ++k) {
+            f[2 * k] = __uint_as_float(w[k] << 16);
+            f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+            mx = fmaxf(mx, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
+          }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          int ex = (int)(__float_as_uint(mx) >> 23) - 127;  // mx in [2^ex, 2^(ex+1))
+          ex = mx == 0.f ? 14 : max(-100, min(ex, 120));
+          const float down = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+          fac[m][hh] = p.scale_log2 * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            qf[m][k][hh] = pack_f16x2(f[4 * k] * down, f[4 * k + 1] * down);
+            qf[m][k][2 + hh] = pack_f16x2(f[4 * k + 2] * down, f[4 * k + 3] * down);
+          }
+        }
+      }
+    end_min = __reduce_min_sync(0xffffffffu, end_min);
+
+    float o[MT][ND][4], mr[MT][2], l[MT][2];
+    int e_ref = 0;  // largest V scale code so far (e4m3)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[m][d][k] = 0.f;
+      mr[m][0] = mr[m][1] = -INFINITY;
+      l[m][0] = l[m][1] = 0.f;
+    }
+
+    // lane's row of tile i in the cache (this head's K plane), -1: none
+    const long long kv_off = (long long)kvh << p.c.page_shift;
+    const uint32_t vpl = p.c.planes == 2 ? L::PLANE : 0;  // V's plane of a stage (K's with shared K = V)
+    const long long v_off = p.c.planes == 2 ? (long long)p.c.kv_heads << p.c.page_shift : 0;
+    auto look = [&](int i) -> long long {
+      const int pos = i * kCaTile + lane;
+      if (i >= t_hi || pos >= s.len) return -1;
+      const long long r = cache_row(p.c, b, pos);
+      if (r < 0) {
+        atomicOr(&g_device_error, kErrPages);
+        return -1;
+      }
+      return r + kv_off;
+    };
+    auto fetch = [&](int i, long long row) {  // tile i, whose lane's row is `row`
+      if (i >= t_hi) return;
+      const uint32_t st = ring + (uint32_t)((i - t_lo) % STAGES) * L::BYTES;
+      constexpr int CH = L::ROW / 16, RPI = 32 / CH;  // 16-byte chunks of a row, rows of one instruction
+#pragma unroll
+      for (int k = 0; k < kCaTile / RPI; ++k) {
+        const int r = k * RPI + lane / CH, ch = lane % CH;
+        const long long src = __shfl_sync(0xffffffffu, row, r);
+        const uint32_t n = src < 0 ? 0u : 16u;
+        const uint8_t* a = pages + (src < 0 ? 0 : src) * L::ROW + ch * 16;
+        cp_async16(st + L::at(r, ch), a, n);
+        if (vpl) cp_async16(st + L::PLANE + L::at(r, ch), a + (src < 0 ? 0 : v_off * L::ROW), n);
+      }
+      if constexpr (FP8) {
+        const long long src = __shfl_sync(0xffffffffu, row, 4 * (lane & 7));
+        if (lane < 16 && src < 0)  // rows in no page are zeros: any scale will do, but not a stale one
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + 2 * L::PLANE + (lane >> 3) * kCaTile + 4 * (lane & 7)), "r"(0u)
+                       : "memory");
+        else if (lane < 16)
+          cp_async4(st + 2 * L::PLANE + (lane >> 3) * kCaTile + 4 * (lane & 7), p.scales + src + (lane >> 3) * v_off);
+      }
+    };
+
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) {
+      fetch(t_lo + i, look(t_lo + i));
+      cp_async_commit();
+    }
+    long long ahead = look(t_lo + STAGES - 1);
+
+    for (int i = t_lo; i < t_hi; ++i) {
+      cp_async_wait<STAGES - 2>();
+      __syncwarp();
+      fetch(i + STAGES - 1, ahead);
+      cp_async_commit();
+      ahead = look(i + STAGES);
+      const uint32_t st = ring + (uint32_t)((i - t_lo) % STAGES) * L::BYTES;
+      const int pos = i * kCaTile;
+
+      // scores
+      float sc[MT][NT][4];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sc[m][j][k] = 0.f;
+      if constexpr (!FP8) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int k = 0; k < KS; k += 2) {
+            uint32_t b0, b1, b2, b3;  // positions 8 j .., d_head 16 k .. 16 k + 31
+            ldsm_x4(st + L::at(8 * j + (lane & 7), 2 * k + (lane >> 3)), b0, b1, b2, b3);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              mma_bf16_16816(sc[m][j], qf[m][k][0], qf[m][k][1], qf[m][k][2], qf[m][k][3], b0, b1);
+              mma_bf16_16816(sc[m][j], qf[m][k + 1][0], qf[m][k + 1][1], qf[m][k + 1][2], qf[m][k + 1][3], b2, b3);
+            }
+          }
+      } else {
+        // column c of n-tile j is position 8 (c / 2) + 2 j + c % 2
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const int r = 8 * (g >> 1) + 2 * j + (g & 1);
+          uint32_t w[KS];
+          if constexpr (DH == 64) {
+            const uint4 v = lds128(st + L::at(r, t));
+            w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+          } else {
+            const uint2 v = lds64(st + L::at(r, t >> 1) + 8 * (t & 1));
+            w[0] = v.x, w[1] = v.y;
+          }
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            const uint32_t b0 = e4m3x2_f16x2((uint16_t)w[k]), b1 = e4m3x2_f16x2((uint16_t)(w[k] >> 16));
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+              mma_f16_16816(sc[m][j], qf[m][k][0], qf[m][k][1], qf[m][k][2], qf[m][k][3], b0, b1);
+          }
+        }
+      }
+
+      // scales: K's into the scores, V's as factors of the weights (8 neighbouring positions a lane)
+      float vf[2 * NT];
+      if constexpr (FP8) {
+        const uint2 kc = lds64(st + 2 * L::PLANE + 8 * t), vc = lds64(st + 2 * L::PLANE + kCaTile + 8 * t);
+        const bool ok = pos + lane < s.len;  // rows past the end hold any code
+        uint32_t code;
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(st + 2 * L::PLANE + kCaTile + lane));
+        const int e_new = max(e_ref, (int)__reduce_max_sync(0xffffffffu, ok ? code : 0u));
+        if (e_new != e_ref) {
+          const float f = e_ref == 0 ? 0.f : fast_exp2((float)(e_ref - e_new));
+          e_ref = e_new;
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[m][d][k] *= f;
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int sh = 8 * ((2 * j + e) & 3);
+            const uint32_t ck = ((j < 2 ? kc.x : kc.y) >> sh) & 0xffu, cv = ((j < 2 ? vc.x : vc.y) >> sh) & 0xffu;
+            const float kf = __uint_as_float(ck << 23);
+            const int d = (int)cv - e_ref + 127 + 7;  // 2^(e - E + 7)
+            vf[2 * j + e] = __uint_as_float((uint32_t)(d < 0 ? 0 : min(d, 134)) << 23);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              sc[m][j][e] *= kf * fac[m][0];
+              sc[m][j][2 + e] *= kf * fac[m][1];
+            }
+          }
+      } else {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc[m][j][k] *= p.scale_log2;
+      }
+      if (pos + kCaTile > end_min) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int x = pos + (FP8 ? 8 * t + 2 * j + (k & 1) : 8 * j + 2 * t + (k & 1));
+              if (x >= end[m][k >> 1]) sc[m][j][k] = -INFINITY;
+            }
+      }
+
+      // running maximum, raised when the tile's exceeds it by kCaLazy; weights as A fragments
+      uint32_t pf[MT][NT][2];
+      bool raise = false;
+      float mn[MT][2];
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          float x = fmaxf(sc[m][0][2 * hh], sc[m][0][2 * hh + 1]);
+#pragma unroll
+          for (int j = 1; j < NT; ++j) x = fmax3(x, sc[m][j][2 * hh], sc[m][j][2 * hh + 1]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          const bool up = x > mr[m][hh] + kCaLazy;
+          mn[m][hh] = up ? x : mr[m][hh];
+          raise |= up;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const float f = mn[m][hh] == mr[m][hh] ? 1.f : fast_exp2(mr[m][hh] - mn[m][hh]);
+            mr[m][hh] = mn[m][hh];
+            l[m][hh] *= f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+              o[m][d][2 * hh] *= f;
+              o[m][d][2 * hh + 1] *= f;
+            }
+          }
+      }
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const float ref = mr[m][hh] == -INFINITY ? 0.f : mr[m][hh];
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            const float w0 = fast_exp2(sc[m][j][2 * hh] - ref), w1 = fast_exp2(sc[m][j][2 * hh + 1] - ref);
+            sum += w0 + w1;
+            if constexpr (FP8) pf[m][j][hh] = pack_f16x2(w0 * vf[2 * j], w1 * vf[2 * j + 1]);
+            else pf[m][j][hh] = pack_bf16x2(w0, w1);
+          }
+          l[m][hh] += sum;
+        }
+
+      // o += weights x V
+#pragma unroll
+      for (int k = 0; k < NT / 2; ++k) {  // 16 positions a step: n-tiles 2 k and 2 k + 1 of the scores
+        if constexpr (!FP8) {
+#pragma unroll
+          for (int d = 0; d < ND; d += 2) {
+            uint32_t b0, b1, b2, b3;
+            ldsm_x4_t(st + vpl + L::at(16 * k + (lane & 15), d + (lane >> 4)), b0, b1, b2, b3);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              mma_bf16_16816(o[m][d], pf[m][2 * k][0], pf[m][2 * k][1], pf[m][2 * k + 1][0], pf[m][2 * k + 1][1], b0, b1);
+              mma_bf16_16816(o[m][d + 1], pf[m][2 * k][0], pf[m][2 * k][1], pf[m][2 * k + 1][0], pf[m][2 * k + 1][1], b2, b3);
+            }
+          }
+        } else {
+          // column n of n-tile d is column n * ND + d of V: a lane's bytes are contiguous
+          uint32_t v[4][ND / 4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = 8 * t + 4 * k + x;
+            if constexpr (DH == 64) {
+              const uint2 w = lds64(st + vpl + L::at(r, g >> 1) + 8 * (g & 1));
+              v[x][0] = w.x;
+              v[x][1] = w.y;
+            } else {
+              v[x][0] = lds32(st + vpl + L::at(r, g >> 2) + 4 * (g & 3));
+            }
+          }
+#pragma unroll
+          for (int d = 0; d < ND; d += 2) {
+            const uint32_t sel = (d & 2) ? 0x7362u : 0x5140u;  // bytes d, d + 1 of the two rows, interleaved
+            const uint32_t lo2 = __byte_perm(v[0][d / 4], v[1][d / 4], sel), hi2 = __byte_perm(v[2][d / 4], v[3][d / 4], sel);
+            const uint32_t b0 = e4m3x2_f16x2((uint16_t)lo2), b1 = e4m3x2_f16x2((uint16_t)hi2);
+            const uint32_t b2 = e4m3x2_f16x2((uint16_t)(lo2 >> 16)), b3 = e4m3x2_f16x2((uint16_t)(hi2 >> 16));
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              mma_f16_16816(o[m][d], pf[m][2 * k][0], pf[m][2 * k][1], pf[m][2 * k + 1][0], pf[m][2 * k + 1][1], b0, b1);
+              mma_f16_16816(o[m][d + 1], pf[m][2 * k][0], pf[m][2 * k][1], pf[m][2 * k + 1][0], pf[m][2 * k + 1][1], b2, b3);
+            }
+          }
+        }
       }
     }
-    float s = 0.f;
+    cp_async_wait<0>();
+    __syncwarp();
+
+    // the item's output where the slice holds all of it, else a partial
+    const bool whole = t_lo == 0 && t_hi == s.units;
+    const long long slot = 2 * gw + (u != u_lo);
+    const float unscale = FP8 ? __uint_as_float((uint32_t)max(e_ref - 7, 0) << 23) : 1.f;
 #pragma unroll
-    for (int k = 0; k < DH; ++k) s = fmaf(q[k], kv[0][k], s);
-    const float mn = fmaxf(m, s), f = fast_exp2(m - mn), w = fast_exp2(s - mn);
-    m = mn;
-    l = l * f + w;
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int k = 0; k < DH; ++k) o[k] = fmaf(o[k], f, w * kv[1][k]);
+      for (int hh = 0; hh < 2; ++hh) {
+        float sum = l[m][hh];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int r = 16 * m + 8 * hh + g;
+        if (r >= n_rows) continue;
+        const float f = whole ? (sum == 0.f ? 0.f : unscale / sum) : unscale;
+        float* po = p.part_o + (slot * BM + r) * DH;
+        const int tok = (r0 + r) / p.group, head = kvh * p.group + (r0 + r) % p.group;
+        __nv_bfloat16* dst = p.a + (long long)(s.first_row + tok) * p.lda + head * DH;
+        // this lane's columns: 8 d + 2 t, + 1 (bf16), or 2 ND t + d, 2 ND t + ND + d (e4m3)
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+          const float x0 = o[m][d][2 * hh] * f, x1 = o[m][d][2 * hh + 1] * f;
+          if constexpr (!FP8) {
+            if (whole) *reinterpret_cast<uint32_t*>(dst + 8 * d + 2 * t) = pack_bf16x2(x0, x1);
+            else *reinterpret_cast<float2*>(po + 8 * d + 2 * t) = make_float2(x0, x1);
+          } else {
+            o[m][d][2 * hh] = x0;
+            o[m][d][2 * hh + 1] = x1;
+          }
+        }
+        if constexpr (FP8) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int d = 0; d < ND; d += 4) {
+              const int col = (2 * t + e) * ND + d;
+              const float x[4] = {o[m][d][2 * hh + e], o[m][d + 1][2 * hh + e], o[m][d + 2][2 * hh + e], o[m][d + 3][2 * hh + e]};
+              if (whole) *reinterpret_cast<uint2*>(dst + col) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+              else *reinterpret_cast<float4*>(po + col) = make_float4(x[0], x[1], x[2], x[3]);
+            }
+        }
+        if (!whole && t == 0)
+          *reinterpret_cast<float2*>(p.part_ml + (slot * BM + r) * 2) = make_float2(mr[m][hh], sum);
+      }
+    u += t_hi - t_lo;
   }
-  float mx = m;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-  const float f = m == -INFINITY ? 0.f : fast_exp2(m - mx);
-  l *= f;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-#pragma unroll
-  for (int k = 0; k < DH; ++k) {
-    float t = o[k] * f;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) t += __shfl_xor_sync(0xffffffffu, t, d);
-    if (lane == k % 32) p.a[row * p.lda + h * DH + k] = __float2bfloat16_rn(l > 0.f ? t / l : 0.f);
+}
+
+// One CTA per (sequence, K|V head, row block): joins the partials of the item, if it was cut.
+constexpr int kCaMergeThreads = 256;
+template <int DH, int BM>
+__global__ void __launch_bounds__(kCaMergeThreads) cache_attend_merge_kernel(const CacheAttnArgs p, int warps) {
+  __shared__ float4 so[kCaMergeThreads];
+  __shared__ float2 sml[kCaMergeThreads];
+  pdl_wait();
+  pdl_trigger();
+  const int qb = blockIdx.x % p.n_qb, kvh = blockIdx.x / p.n_qb % p.c.kv_heads, b = blockIdx.x / (p.n_qb * p.c.kv_heads);
+  const CaSeq s = ca_seq(p, b, BM);
+  if (qb >= s.blocks) return;
+  const long long T = p.before[p.c.B], W = ca_workers(T, warps);
+  const long long u0 = p.before[b] + (long long)(kvh * s.blocks + qb) * s.units, u1 = u0 + s.units - 1;
+  const long long w0 = ((u0 + 1) * W - 1) / T, w1 = ((u1 + 1) * W - 1) / T;
+  if (w0 == w1) return;
+  const int n_rows = min(BM, s.take * p.group - qb * BM), n = (int)(w1 - w0 + 1);
+  const int vecs = n_rows * (DH / 4);
+  // `groups` threads take every groups-th partial of one vector of 4 columns
+  int groups = 1;
+  while (groups * 2 * vecs <= kCaMergeThreads && groups < n) groups *= 2;
+  const int per = kCaMergeThreads / groups, grp = threadIdx.x / per;
+  for (int v0 = 0; v0 < vecs; v0 += per) {
+    const int v = v0 + threadIdx.x % per;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int r = v / (DH / 4), c4 = v % (DH / 4);
+    if (v < vecs) {
+#pragma unroll 4
+      for (int k = grp; k < n; k += groups) {
+        const long long w = w0 + k;
+        const long long slot = (2 * w + (w * T / W < u0 ? 1 : 0)) * BM + r;
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot * 2);
+        const float4 x = *reinterpret_cast<const float4*>(p.part_o + slot * DH + 4 * c4);
+        const float mn = fmaxf(m, ml.x);
+        const float fo = m == mn ? 1.f : fast_exp2(m - mn), fx = ml.x == mn ? 1.f : fast_exp2(ml.x - mn);
+        m = mn;
+        l = l * fo + ml.y * fx;
+        o.x = o.x * fo + x.x * fx;
+        o.y = o.y * fo + x.y * fx;
+        o.z = o.z * fo + x.z * fx;
+        o.w = o.w * fo + x.w * fx;
+      }
+    }
+    if (groups > 1) {  // one round: vecs <= per
+      so[threadIdx.x] = o;
+      sml[threadIdx.x] = make_float2(m, l);
+      __syncthreads();
+      if (grp == 0 && v < vecs)
+        for (int k = 1; k < groups; ++k) {
+          const float2 ml = sml[k * per + v];
+          const float4 x = so[k * per + v];
+          const float mn = fmaxf(m, ml.x);
+          const float fo = m == mn ? 1.f : fast_exp2(m - mn), fx = ml.x == mn ? 1.f : fast_exp2(ml.x - mn);
+          m = mn;
+          l = l * fo + ml.y * fx;
+          o.x = o.x * fo + x.x * fx;
+          o.y = o.y * fo + x.y * fx;
+          o.z = o.z * fo + x.z * fx;
+          o.w = o.w * fo + x.w * fx;
+        }
+    }
+    if (grp == 0 && v < vecs) {
+      const float f = l == 0.f ? 0.f : 1.f / l;
+      const int row = qb * BM + r, tok = row / p.group, head = kvh * p.group + row % p.group;
+      *reinterpret_cast<uint2*>(p.a + (long long)(s.first_row + tok) * p.lda + head * DH + 4 * c4) =
+          make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+    }
   }
 }
 

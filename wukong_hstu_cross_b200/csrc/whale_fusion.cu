@@ -2716,6 +2716,41 @@ whale_status launch_rows(bool append, const RowsArgs& a, cudaStream_t st) {
                     dim3(kRowsThreads), 0, st, a);
 }
 
+// Row blocks and workspace of the attention over the cache.
+struct CacheAttnPlan {
+  int bm, n_qb, max_new;
+  size_t ml_off, before_off, bytes;
+};
+whale_status plan_cache_attention(const Shape& s, const whale_cache& k, const whale_chunk& c, CacheAttnPlan* p) {
+  const int group = s.h / k.n_kv_heads;
+  p->max_new = (int)std::min<long long>(c.max_new, c.total_new);
+  const long long rows = (long long)p->max_new * group;
+  p->bm = rows <= 16 ? 16 : 32;
+  // rows and positions are counted in 32 bits in the kernels
+  if (c.total_new * s.h >= (1ll << 31) || c.max_length > (1 << 30)) return WHALE_ERR_UNSUPPORTED;
+  p->n_qb = (int)std::max(1ll, cdiv<long long>(rows, p->bm));
+  if ((double)c.B * k.n_kv_heads * p->n_qb >= 2147483647.0) return WHALE_ERR_UNSUPPORTED;
+  const size_t slots = 2 * (size_t)kNumSM * kCaWarps;
+  p->ml_off = align_up(slots * p->bm * s.dh * 4);
+  p->before_off = p->ml_off + align_up(slots * p->bm * 8);
+  p->bytes = p->before_off + align_up(((size_t)c.B + 1) * 8);
+  return WHALE_OK;
+}
+
+template <int DH, bool FP8, int MT>
+whale_status launch_attend_rows_t(const CacheAttnArgs& a, cudaStream_t st) {
+  auto kern = cache_attend_kernel<DH, FP8, MT>;
+  constexpr int smem = CaTile<DH, FP8>::SMEM;
+  CUCHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  WCHECK(launch_pdl(kern, dim3(kNumSM), dim3(kCaThreads), smem, st, a));
+  return launch_pdl(cache_attend_merge_kernel<DH, 16 * MT>, dim3((unsigned)(a.c.B * a.c.kv_heads * a.n_qb)),
+                    dim3(kCaMergeThreads), 0, st, a, kNumSM * kCaWarps);
+}
+template <int DH, bool FP8>
+whale_status launch_attend_rows(const CacheAttnPlan& p, const CacheAttnArgs& a, cudaStream_t st) {
+  return p.bm == 16 ? launch_attend_rows_t<DH, FP8, 1>(a, st) : launch_attend_rows_t<DH, FP8, 2>(a, st);
+}
+
 whale_status cache_rows_call(const whale_config* cfg, const whale_cache* cache, const whale_chunk* chunk,
                              const void* src, void* dst, long long ld, whale_stream_t stream) {
   Shape s;
@@ -2854,8 +2889,11 @@ whale_status whale_cache_read(const whale_config* cfg, const whale_cache* cache,
 size_t whale_cache_attention_workspace_size(const whale_config* cfg, const whale_cache* cache,
                                             const whale_chunk* chunk) {
   Shape s;
-  if (check_cache(cfg, cache, &s) != WHALE_OK || check_chunk(chunk) != WHALE_OK) return 0;
-  return kAlign;
+  CacheAttnPlan p;
+  if (check_cache(cfg, cache, &s) != WHALE_OK || check_chunk(chunk) != WHALE_OK ||
+      plan_cache_attention(s, *cache, *chunk, &p) != WHALE_OK)
+    return 0;
+  return p.bytes;
 }
 
 whale_status whale_cache_attention(const whale_config* cfg, const whale_cache* cache, const whale_chunk* chunk,
@@ -2871,9 +2909,9 @@ whale_status whale_cache_attention(const whale_config* cfg, const whale_cache* c
   if (empty) return WHALE_OK;
   if (!q || !a || !aligned16(q) || !aligned16(a) || ld_q % 8 || ld_a % 8 || ld_q < s.d || ld_a < s.d)
     return WHALE_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < whale_cache_attention_workspace_size(cfg, cache, chunk) ||
-      (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)))
-    return WHALE_ERR_WORKSPACE;
+  CacheAttnPlan plan;
+  WCHECK(plan_cache_attention(s, *cache, *chunk, &plan));
+  if (!ws || ws_bytes < plan.bytes || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return WHALE_ERR_WORKSPACE;
   CacheAttnArgs p{};
   p.c = chunk_view(s, *cache, *chunk);
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -2885,15 +2923,16 @@ whale_status whale_cache_attention(const whale_config* cfg, const whale_cache* c
   p.heads = s.h;
   p.group = s.h / cache->n_kv_heads;
   p.causal = flags & WHALE_ATTEND_CAUSAL ? 1 : 0;
-  p.scale_log2 = scale_log2_of(s);
+  p.max_new = plan.max_new;
+  p.n_qb = plan.n_qb;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s.dh));
+  p.part_o = static_cast<float*>(ws);
+  p.part_ml = p.part_o + plan.ml_off / 4;
+  p.before = reinterpret_cast<long long*>(static_cast<uint8_t*>(ws) + plan.before_off);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const dim3 grid((unsigned)cdiv<long long>(chunk->total_new * s.h, 4));
   const bool fp8 = cache->format == WHALE_CACHE_E4M3;
-  if (s.dh == 32)
-    return launch_pdl(fp8 ? cache_attend_simple_kernel<32, true> : cache_attend_simple_kernel<32, false>, grid,
-                      dim3(128), 0, st, p);
-  return launch_pdl(fp8 ? cache_attend_simple_kernel<64, true> : cache_attend_simple_kernel<64, false>, grid, dim3(128),
-                    0, st, p);
+  if (s.dh == 32) return fp8 ? launch_attend_rows<32, true>(plan, p, st) : launch_attend_rows<32, false>(plan, p, st);
+  return fp8 ? launch_attend_rows<64, true>(plan, p, st) : launch_attend_rows<64, false>(plan, p, st);
 }
 
 whale_status whale_test_bounded_waits(unsigned long long limit_ns, whale_stream_t stream) {
