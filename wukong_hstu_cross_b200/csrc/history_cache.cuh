@@ -44,18 +44,24 @@ struct RowsArgs {
 };
 
 constexpr int kRowsThreads = 256;
+constexpr int kRowsHeads = 8;  // heads whose 16 bytes a lane has in flight at once
 
-// Append: a row's d_head / 8 lanes take its heads one after another, 16 bytes a lane; the amax of a head is
-// log2(lanes) shuffles. HBM-bound: each number is read once and written once.
+// Append: a row's d_head / 8 lanes take its heads one after another, 16 bytes a lane, the first kRowsHeads loaded
+// before the row's place in the cache is looked up; the amax of a head is log2(lanes) shuffles. HBM-bound: each
+// number is read once and written once.
 template <int DH, bool FP8>
 __global__ void __launch_bounds__(kRowsThreads) cache_append_kernel(const RowsArgs a) {
-  constexpr int LPH = DH / 8, RPW = 32 / LPH;
+  constexpr int LPH = DH / 8, RPW = 32 / LPH, HU = kRowsHeads;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, li = lane % LPH;
   const long long row = ((long long)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5)) * RPW + lane / LPH;
   const int heads = a.c.planes * a.c.kv_heads;
-  const bool mine = a.c.B > 0 && row < a.c.total && row < a.c.offsets[a.c.B];
+  const bool mine = row < a.c.total && row < a.c.offsets[a.c.B];
+  const uint4* src = reinterpret_cast<const uint4*>(a.src + (mine ? row : 0) * a.ld) + li;
+  uint4 w[HU];
+#pragma unroll
+  for (int u = 0; u < HU; ++u) w[u] = mine && u < heads ? src[u * LPH] : make_uint4(0u, 0u, 0u, 0u);
   long long at = -1;
   if (mine) {
     const int b = chunk_seq(a.c, row);
@@ -64,72 +70,95 @@ __global__ void __launch_bounds__(kRowsThreads) cache_append_kernel(const RowsAr
   }
   const bool live = at >= 0;
   if (!__any_sync(0xffffffffu, live)) return;
-  const uint4* src = reinterpret_cast<const uint4*>(a.src + (live ? row : 0) * a.ld) + li;
-  for (int h = 0; h < heads; ++h) {
-    const long long out = at + ((long long)h << a.c.page_shift);
-    const uint4 w = live ? src[h * LPH] : make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (!FP8) {
-      if (live) *reinterpret_cast<uint4*>(a.pages + (out * DH + li * 8) * 2) = w;
-    } else {
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-      float f[8], m = 0.f;
+  for (int h0 = 0; h0 < heads; h0 += HU) {
+    uint4 nx[HU];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        f[2 * k] = __uint_as_float(u[k] << 16);
-        f[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-        m = fmaxf(m, fmaxf(fabsf(f[2 * k]), fabsf(f[2 * k + 1])));
-      }
+    for (int u = 0; u < HU; ++u)
+      nx[u] = mine && h0 + HU + u < heads ? src[(h0 + HU + u) * LPH] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int o = LPH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const int e = scale_exponent(m);
-      const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-      uint32_t q[2];
+    for (int k = 0; k < HU; ++k) {
+      if (h0 + k >= heads) break;
+      const long long out = at + ((long long)(h0 + k) << a.c.page_shift);
+      if constexpr (!FP8) {
+        if (live) *reinterpret_cast<uint4*>(a.pages + (out * DH + li * 8) * 2) = w[k];
+      } else {
+        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+        float f[8], m = 0.f;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        q[k] = (uint32_t)e4m3x2(f[4 * k] * inv, f[4 * k + 1] * inv) |
-               ((uint32_t)e4m3x2(f[4 * k + 2] * inv, f[4 * k + 3] * inv) << 16);
-      if (live) {
-        *reinterpret_cast<uint2*>(a.pages + out * DH + li * 8) = make_uint2(q[0], q[1]);
-        if (li == 0) a.scales[out] = (uint8_t)(e + 127);
+        for (int i = 0; i < 4; ++i) {
+          f[2 * i] = __uint_as_float(u[i] << 16);
+          f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+          m = fmaxf(m, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
+        }
+#pragma unroll
+        for (int o = LPH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const int e = scale_exponent(m);
+        const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+        uint32_t q[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          q[i] = (uint32_t)e4m3x2(f[4 * i] * inv, f[4 * i + 1] * inv) |
+                 ((uint32_t)e4m3x2(f[4 * i + 2] * inv, f[4 * i + 3] * inv) << 16);
+        if (live) {
+          *reinterpret_cast<uint2*>(a.pages + out * DH + li * 8) = make_uint2(q[0], q[1]);
+          if (li == 0) a.scales[out] = (uint8_t)(e + 127);
+        }
       }
     }
+#pragma unroll
+    for (int u = 0; u < HU; ++u) w[u] = nx[u];
   }
 }
 
 // Read: the same lanes the other way; rows in no page come back as zeros.
 template <int DH, bool FP8>
 __global__ void __launch_bounds__(kRowsThreads) cache_read_kernel(const RowsArgs a) {
-  constexpr int LPH = DH / 8, RPW = 32 / LPH;
+  constexpr int LPH = DH / 8, RPW = 32 / LPH, HU = kRowsHeads;
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, li = lane % LPH;
   const long long row = ((long long)blockIdx.x * (kRowsThreads / 32) + (threadIdx.x >> 5)) * RPW + lane / LPH;
   const int heads = a.c.planes * a.c.kv_heads;
-  if (a.c.B <= 0 || row >= a.c.total || row >= a.c.offsets[a.c.B]) return;
+  if (row >= a.c.total || row >= a.c.offsets[a.c.B]) return;
   const int b = chunk_seq(a.c, row);
   const long long at = cache_row(a.c, b, (long long)a.c.lengths[b] - (a.c.offsets[b + 1] - row));
   if (at < 0) atomicOr(&g_device_error, kErrPages);
   uint4* dst = reinterpret_cast<uint4*>(a.dst + row * a.ld) + li;
-  for (int h = 0; h < heads; ++h) {
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (at >= 0) {
-      const long long in = at + ((long long)h << a.c.page_shift);
-      if constexpr (!FP8) {
-        w = *reinterpret_cast<const uint4*>(a.pages + (in * DH + li * 8) * 2);
-      } else {
-        const uint2 q = *reinterpret_cast<const uint2*>(a.pages + in * DH + li * 8);
-        const float sc = __uint_as_float((uint32_t)a.scales[in] << 23);
-        uint32_t o[4];
+  for (int h0 = 0; h0 < heads; h0 += HU) {
+    uint4 w[HU];
+    uint32_t sc[HU];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t v = e4m3x2_f16x2((uint16_t)((k < 2 ? q.x : q.y) >> (16 * (k & 1))));
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
-          o[k] = pack_bf16x2(f.x * sc, f.y * sc);
+    for (int k = 0; k < HU; ++k) {
+      w[k] = make_uint4(0u, 0u, 0u, 0u);
+      sc[k] = 0u;
+      if (at >= 0 && h0 + k < heads) {
+        const long long in = at + ((long long)(h0 + k) << a.c.page_shift);
+        if constexpr (!FP8) {
+          w[k] = *reinterpret_cast<const uint4*>(a.pages + (in * DH + li * 8) * 2);
+        } else {
+          const uint2 q = *reinterpret_cast<const uint2*>(a.pages + in * DH + li * 8);
+          w[k].x = q.x;
+          w[k].y = q.y;
+          sc[k] = a.scales[in];
         }
-        w = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
-    dst[h * LPH] = w;
+#pragma unroll
+    for (int k = 0; k < HU; ++k) {
+      if (h0 + k >= heads) break;
+      if constexpr (FP8) {
+        const float f = __uint_as_float(sc[k] << 23);
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t v = e4m3x2_f16x2((uint16_t)((i < 2 ? w[k].x : w[k].y) >> (16 * (i & 1))));
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v));
+          o[i] = pack_bf16x2(x.x * f, x.y * f);
+        }
+        w[k] = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+      dst[(h0 + k) * LPH] = w[k];
+    }
   }
 }
 

@@ -7,13 +7,15 @@
 //   dg = sum over rows and heads of dn * x * r
 //   dx = r * (dn * g) - x * r^3 * mean(dn * g * x)
 //
-// Work split. A head is LPH = d_head / V lanes of V = 16 bytes of columns each, and those LPH lanes take
-// one row and walk its heads: the angles of a row are the same for every head, so each pair's sine and
-// cosine is formed once per row (V / 2 pairs a lane, handed round by shuffles in the halves layout)
-// and the gains stay in registers. A warp's lanes cover 32 / LPH rows; a head's columns are one 64- or
-// 128-byte segment, so loads and stores are whole sectors. Everything is held in fp32 and rounded once, at
-// the store. Angles are reduced in fp64, in turns: p times base^(-2i/rot) / 2 pi keeps 2^-53 of the
-// product where fp32 would lose the angle of a far position.
+// Work split. A head is LPH = d_head / V lanes of V columns (16 bytes) each, and those LPH lanes take one row
+// and walk its heads: the angles of a row are the same for every head, so each sine and cosine is formed once per
+// row, by the lane that uses it, and multiplied into the gains. A lane holds both columns of its V / 2 pairs
+// (halves layout: two 8-byte pieces rot / 2 apart), so nothing passes between lanes but the sum of squares. A
+// warp's lanes cover 32 / LPH rows; a head's columns are one segment of 32 bytes or more, so loads and stores are whole
+// sectors. The next kNrHeads heads (the next row's first ones at a row's end) are loaded before the
+// present ones are used. Everything is held in fp32 and rounded once, at the store. Angles are reduced
+// in fp64, in turns: p times base^(-2i/rot) / 2 pi keeps 2^-53 of the product where fp32 would lose the angle of a
+// far position.
 #pragma once
 
 #include "ptx.cuh"
@@ -42,38 +44,62 @@ struct NrArgs {
   double turns[kNrMaxPairs];  // base^(-2 i / rot) / (2 pi)
 };
 
-// 16 bytes of columns as fp32.
-template <typename T>
-struct NrVec;
-template <>
-struct NrVec<__nv_bfloat16> {
-  static constexpr int V = 8;
-  static __device__ __forceinline__ void unpack(const uint4& w, float (&f)[8]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+// V columns of a lane as fp32, read and written as two pieces of C = V / 2 columns.
+template <typename T, int V>
+struct NrRaw {
+  uint32_t w[V * sizeof(T) / 4];
+};
+template <typename T, int V>
+__device__ __forceinline__ NrRaw<T, V> nr_load(const T* row, int o1, int o2, bool whole) {
+  NrRaw<T, V> r;
+  constexpr int N = V * sizeof(T) / 4;  // words: 4, or 8 (fp32 gradients of bf16 rows)
+  if constexpr (N == 4) {
+    if (whole) {
+      const uint4 a = *reinterpret_cast<const uint4*>(row + o1);
+      r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+    } else {
+      const uint2 a = *reinterpret_cast<const uint2*>(row + o1), b = *reinterpret_cast<const uint2*>(row + o2);
+      r.w[0] = a.x, r.w[1] = a.y, r.w[2] = b.x, r.w[3] = b.y;
+    }
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(row + o1), b = *reinterpret_cast<const uint4*>(row + o2);
+    r.w[0] = a.x, r.w[1] = a.y, r.w[2] = a.z, r.w[3] = a.w;
+    r.w[4] = b.x, r.w[5] = b.y, r.w[6] = b.z, r.w[7] = b.w;
+  }
+  return r;
+}
+template <typename T, int V>
+__device__ __forceinline__ void nr_unpack(const NrRaw<T, V>& r, float (&f)[V]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(u[i] << 16);
-      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  for (int i = 0; i < V; ++i) {
+    if constexpr (sizeof(T) == 4) f[i] = __uint_as_float(r.w[i]);
+    else f[i] = __uint_as_float(i & 1 ? r.w[i / 2] & 0xffff0000u : r.w[i / 2] << 16);
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void nr_store(T* row, int o1, int o2, bool whole, const float (&f)[V]) {
+  uint32_t w[V * sizeof(T) / 4];
+#pragma unroll
+  for (int i = 0; i < V; i += 2) {
+    if constexpr (sizeof(T) == 4) {
+      w[i] = __float_as_uint(f[i]);
+      w[i + 1] = __float_as_uint(f[i + 1]);
+    } else {
+      w[i / 2] = pack_bf16x2(f[i], f[i + 1]);
     }
   }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                      pack_bf16x2(f[6], f[7]));
+  if constexpr (V * sizeof(T) == 16) {
+    if (whole) {
+      *reinterpret_cast<uint4*>(row + o1) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      *reinterpret_cast<uint2*>(row + o1) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(row + o2) = make_uint2(w[2], w[3]);
+    }
+  } else {
+    *reinterpret_cast<uint4*>(row + o1) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(row + o2) = make_uint4(w[4], w[5], w[6], w[7]);
   }
-};
-template <>
-struct NrVec<float> {
-  static constexpr int V = 4;
-  static __device__ __forceinline__ void unpack(const uint4& w, float (&f)[4]) {
-    f[0] = __uint_as_float(w.x);
-    f[1] = __uint_as_float(w.y);
-    f[2] = __uint_as_float(w.z);
-    f[3] = __uint_as_float(w.w);
-  }
-  static __device__ __forceinline__ uint4 pack(const float (&f)[4]) {
-    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
-  }
-};
+}
 
 template <int LPH>
 __device__ __forceinline__ float nr_sum(float v) {
@@ -82,154 +108,132 @@ __device__ __forceinline__ float nr_sum(float v) {
   return v;
 }
 
-// Sines and cosines that this lane's V columns need, as full-length factors: with w the other column of
-// the pair, the rotated column is c * own + s * w. Columns that do not turn get (1, 0).
-//  halves:   column e < rot/2 pairs with e + rot/2, held by the lane `hop` lanes on (or back)
-//  adjacent: columns 2 i and 2 i + 1 pair, both in this lane; c and s are per pair there
-template <int V, int LPH, bool ADJ>
-__device__ __forceinline__ void nr_angles(const NrArgs& a, int p, int li, float (&c)[ADJ ? V / 2 : V],
-                                          float (&s)[ADJ ? V / 2 : V], int hop) {
-  float mc[V / 2], ms[V / 2];
+// Where a lane's columns are: pieces [o1, o1 + V/2) and [o2, o2 + V/2) of the head. Pair k of the lane is
+// (f[k], f[V/2 + k]) in the halves layout, (f[2k], f[2k+1]) in the adjacent one; it is pair first + k of the head, and turns if
+// that is below rot / 2. Columns past rot come in the same form and do not turn.
+struct NrLane {
+  int o1, o2, first;
+};
+template <int V, bool ADJ>
+__device__ __forceinline__ NrLane nr_lane(int rot, int li) {
+  constexpr int C = V / 2;
+  NrLane l;
+  l.first = li * C;
+  const bool turns = !ADJ && l.first < rot / 2;
+  l.o1 = turns ? l.first : (ADJ ? li * V : rot + (l.first - rot / 2) * 2);
+  l.o2 = turns ? rot / 2 + l.first : l.o1 + C;
+  return l;
+}
+template <bool ADJ, int V>
+__device__ __forceinline__ constexpr int nr_a(int k) { return ADJ ? 2 * k : k; }
+template <bool ADJ, int V>
+__device__ __forceinline__ constexpr int nr_b(int k) { return ADJ ? 2 * k + 1 : V / 2 + k; }
+
+template <int C>
+__device__ __forceinline__ void nr_angles(const NrArgs& a, int p, int first, float (&c)[C], float (&s)[C]) {
 #pragma unroll
-  for (int k = 0; k < V / 2; ++k) {
-    const int i = li * (V / 2) + k;
-    mc[k] = 1.f;
-    ms[k] = 0.f;
-    if (i < a.rot / 2) {
-      const double t = (double)p * a.turns[i];
-      sincospif((float)(2.0 * (t - rint(t))), &ms[k], &mc[k]);
-    }
-  }
-  if constexpr (ADJ) {
-#pragma unroll
-    for (int k = 0; k < V / 2; ++k) {
-      c[k] = mc[k];
-      s[k] = ms[k];
-    }
-  } else {
-    // columns e0 .. e0 + V - 1 of pairs (e mod rot/2): formed by lanes 2 l' and 2 l' + 1 of the head
-    const int l2 = li < hop ? li : li - hop;  // lane of the pair's first column
-    const bool turns = li < 2 * hop;
-    const int base = (threadIdx.x & 31 & ~(LPH - 1)) + ((2 * l2) & (LPH - 1));
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int src = base + (k >= V / 2 ? 1 : 0);
-      const float cc = __shfl_sync(0xffffffffu, mc[k % (V / 2)], src);
-      const float ss = __shfl_sync(0xffffffffu, ms[k % (V / 2)], src);
-      c[k] = turns ? cc : 1.f;
-      s[k] = turns ? (li < hop ? -ss : ss) : 0.f;
+  for (int k = 0; k < C; ++k) {
+    c[k] = 1.f;
+    s[k] = 0.f;
+    if (first + k < a.rot / 2) {
+      const double t = (double)p * a.turns[first + k];
+      sincospif((float)(2.0 * (t - rint(t))), &s[k], &c[k]);
     }
   }
 }
 
-// y = rotation of n by the factors of nr_angles, `w` = the partner lane's columns (halves layout only)
-template <int V, bool ADJ, bool BACK>
-__device__ __forceinline__ void nr_turn(const float (&n)[V], const float (&w)[V], const float (&c)[ADJ ? V / 2 : V],
-                                        const float (&s)[ADJ ? V / 2 : V], float (&y)[V]) {
-  if constexpr (ADJ) {
+template <typename T, int V>
+__device__ __forceinline__ void nr_gains(const float* gain, const NrLane& l, float (&g)[V]) {
 #pragma unroll
-    for (int k = 0; k < V / 2; ++k) {
-      const float sn = BACK ? -s[k] : s[k];
-      y[2 * k] = n[2 * k] * c[k] - n[2 * k + 1] * sn;
-      y[2 * k + 1] = n[2 * k] * sn + n[2 * k + 1] * c[k];
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < V; ++k) y[k] = n[k] * c[k] + w[k] * (BACK ? -s[k] : s[k]);
+  for (int k = 0; k < V / 2; ++k) {
+    g[k] = gain[l.o1 + k];
+    g[V / 2 + k] = gain[l.o2 + k];
   }
 }
+
+constexpr int kNrHeads = 4;
 
 template <typename T, int DH, bool ADJ>
 __global__ void __launch_bounds__(kNrThreads) norm_rotate_kernel(const __grid_constant__ NrArgs a) {
-  constexpr int V = NrVec<T>::V, LPH = DH / V, RPW = 32 / LPH, HU = 4;
+  constexpr int V = 16 / sizeof(T), C = V / 2, LPH = DH / V, RPW = 32 / LPH, HU = kNrHeads, WARPS = kNrThreads / 32;
   pdl_wait();
   pdl_trigger();
   const int second = blockIdx.x >= (unsigned)a.blocks0;
   const NrPart& p = a.part[second];
   const int block = second ? blockIdx.x - a.blocks0 : blockIdx.x;
+  const int blocks = second ? gridDim.x - a.blocks0 : a.blocks0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int li = lane % LPH;
-  const int hop = a.rot / 2 / V;
-  const long long row = ((long long)block * (kNrThreads / 32) + warp) * RPW + lane / LPH;
-  const bool live = row < p.rows;  // every lane keeps step: the shuffles need the whole warp
-  const long long r0 = live ? row : 0;
-  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + r0 * p.ldx) + li;
-  uint4* y = reinterpret_cast<uint4*>(static_cast<T*>(p.y) + r0 * p.ldy) + li;
-  if (row - lane / LPH >= p.rows) return;  // a whole warp past the end
-  uint4 w[HU];
+  const NrLane l = nr_lane<V, ADJ>(a.rot, lane % LPH);
+  const bool whole = l.o2 == l.o1 + C;
+  const long long step = (long long)blocks * WARPS * RPW;
+  long long base = ((long long)block * WARPS + warp) * RPW;
+  if (base >= p.rows) return;
+  long long row = base + lane / LPH;  // past the end: the last row, not stored (the shuffles need the whole warp)
+  auto src_of = [&](long long r) { return static_cast<const T*>(p.x) + (r < p.rows ? r : p.rows - 1) * p.ldx; };
+  const T* x = src_of(row);
+  NrRaw<T, V> w[HU], nx[HU];
 #pragma unroll
   for (int u = 0; u < HU; ++u)
-    if (live && u < p.heads) w[u] = x[u * LPH];
-  float g[V], gw[V];  // gains of this lane's columns and of their partners
-  const bool turns = !ADJ && li < 2 * hop;
-  const int partner = turns ? (li < hop ? lane + hop : lane - hop) : lane;
-  const int le = turns ? (li < hop ? li + hop : li - hop) : li;
+    if (u < p.heads) w[u] = nr_load<T, V>(x + u * DH, l.o1, l.o2, whole);
+  int pos = p.pos[row < p.rows ? row : p.rows - 1];
+  float g[V];
+  nr_gains<T, V>(p.gain, l, g);
+  for (; base < p.rows; base += step) {
+    row = base + lane / LPH;
+    const bool live = row < p.rows, more = base + step < p.rows;
+    T* y = static_cast<T*>(p.y) + (live ? row : 0) * p.ldy;
+    const T* next = src_of(row + step);
+    const int next_pos = more ? p.pos[row + step < p.rows ? row + step : p.rows - 1] : 0;
+    // turn and gain in one: y_a = r (a ca - b sb), y_b = r (a sa + b cb)
+    float ca[C], sa[C], cb[C], sb[C];
+    {
+      float c[C], s[C];
+      nr_angles<C>(a, pos, l.first, c, s);
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    g[k] = p.gain[li * V + k];
-    gw[k] = p.gain[le * V + k];
-  }
-  float c[ADJ ? V / 2 : V], s[ADJ ? V / 2 : V];
-  nr_angles<V, LPH, ADJ>(a, live ? p.pos[row] : 0, li, c, s, hop);
-  for (int h0 = 0; h0 < p.heads; h0 += HU) {
-    uint4 nx[HU];
+      for (int k = 0; k < C; ++k) {
+        const float ga = g[nr_a<ADJ, V>(k)], gb = g[nr_b<ADJ, V>(k)];
+        ca[k] = c[k] * ga;
+        sa[k] = s[k] * ga;
+        cb[k] = c[k] * gb;
+        sb[k] = s[k] * gb;
+      }
+    }
+    for (int h0 = 0; h0 < p.heads; h0 += HU) {
+      const bool last = h0 + HU >= p.heads;
 #pragma unroll
-    for (int u = 0; u < HU; ++u)
-      if (live && h0 + HU + u < p.heads) nx[u] = x[(h0 + HU + u) * LPH];
-#pragma unroll
-    for (int u = 0; u < HU; ++u) {
-      if (h0 + u >= p.heads) break;
-      float f[V], v[V], out[V];
-      NrVec<T>::unpack(w[u], f);
-      float q = 0.f;
-#pragma unroll
-      for (int k = 0; k < V; ++k) q = fmaf(f[k], f[k], q);
-      const float r = rsqrtf(nr_sum<LPH>(q) * (1.0f / DH) + a.eps);
-      if constexpr (!ADJ) {
-        uint4 o;
-        o.x = __shfl_sync(0xffffffffu, w[u].x, partner);
-        o.y = __shfl_sync(0xffffffffu, w[u].y, partner);
-        o.z = __shfl_sync(0xffffffffu, w[u].z, partner);
-        o.w = __shfl_sync(0xffffffffu, w[u].w, partner);
-        NrVec<T>::unpack(o, v);
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[k] *= r * gw[k];
+      for (int u = 0; u < HU; ++u) {
+        if (!last) {
+          if (h0 + HU + u < p.heads) nx[u] = nr_load<T, V>(x + (h0 + HU + u) * DH, l.o1, l.o2, whole);
+        } else if (more && u < p.heads) {
+          nx[u] = nr_load<T, V>(next + u * DH, l.o1, l.o2, whole);
+        }
       }
 #pragma unroll
-      for (int k = 0; k < V; ++k) f[k] *= r * g[k];
-      nr_turn<V, ADJ, false>(f, v, c, s, out);
-      if (live) y[(h0 + u) * LPH] = NrVec<T>::pack(out);
+      for (int u = 0; u < HU; ++u) {
+        if (h0 + u < p.heads) {
+          float f[V], out[V];
+          nr_unpack<T, V>(w[u], f);
+          float q0 = 0.f, q1 = 0.f;
+#pragma unroll
+          for (int k = 0; k < V; k += 2) {
+            q0 = fmaf(f[k], f[k], q0);
+            q1 = fmaf(f[k + 1], f[k + 1], q1);
+          }
+          const float r = rsqrtf(nr_sum<LPH>(q0 + q1) * (1.0f / DH) + a.eps);
+#pragma unroll
+          for (int k = 0; k < C; ++k) {
+            const float xa = f[nr_a<ADJ, V>(k)], xb = f[nr_b<ADJ, V>(k)];
+            out[nr_a<ADJ, V>(k)] = (xa * ca[k] - xb * sb[k]) * r;
+            out[nr_b<ADJ, V>(k)] = (xa * sa[k] + xb * cb[k]) * r;
+          }
+          if (live) nr_store<T, V>(y + (h0 + u) * DH, l.o1, l.o2, whole, out);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < HU; ++u) w[u] = nx[u];
     }
-#pragma unroll
-    for (int u = 0; u < HU; ++u) w[u] = nx[u];
-  }
-}
-
-// Gradient rows as fp32, V columns of a lane.
-template <typename GT, int V>
-__device__ __forceinline__ void nr_load_grad(const GT* row, int col, float (&f)[V]) {
-  if constexpr (sizeof(GT) == 4) {
-#pragma unroll
-    for (int k = 0; k < V / 4; ++k) {
-      const float4 t = *reinterpret_cast<const float4*>(row + col + 4 * k);
-      f[4 * k] = t.x;
-      f[4 * k + 1] = t.y;
-      f[4 * k + 2] = t.z;
-      f[4 * k + 3] = t.w;
-    }
-  } else {
-    static_assert(sizeof(GT) == 4 || V == 8, "bf16 gradients come with bf16 rows");
-    NrVec<__nv_bfloat16>::unpack(*reinterpret_cast<const uint4*>(row + col), f);
-  }
-}
-template <typename GT, int V>
-__device__ __forceinline__ void nr_store_grad(GT* row, int col, const float (&f)[V]) {
-  if constexpr (sizeof(GT) == 4) {
-#pragma unroll
-    for (int k = 0; k < V / 4; ++k)
-      *reinterpret_cast<float4*>(row + col + 4 * k) = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
-  } else {
-    *reinterpret_cast<uint4*>(row + col) = NrVec<__nv_bfloat16>::pack(f);
+    x = next;
+    pos = next_pos;
   }
 }
 
@@ -238,7 +242,7 @@ __device__ __forceinline__ void nr_store_grad(GT* row, int col, const float (&f)
 // fixed order).
 template <typename T, typename GT, int DH, bool ADJ>
 __global__ void __launch_bounds__(kNrThreads) norm_rotate_backward_kernel(const __grid_constant__ NrArgs a) {
-  constexpr int V = NrVec<T>::V, LPH = DH / V, RPW = 32 / LPH, WARPS = kNrThreads / 32;
+  constexpr int V = 16 / sizeof(T), C = V / 2, LPH = DH / V, RPW = 32 / LPH, WARPS = kNrThreads / 32, HU = 2;
   __shared__ float sums[WARPS][DH];
   pdl_wait();
   pdl_trigger();
@@ -247,61 +251,79 @@ __global__ void __launch_bounds__(kNrThreads) norm_rotate_backward_kernel(const 
   const int block = second ? blockIdx.x - a.blocks0 : blockIdx.x;
   const int blocks = second ? gridDim.x - a.blocks0 : a.blocks0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int li = lane % LPH;
-  const int hop = a.rot / 2 / V;
-  const bool turns = !ADJ && li < 2 * hop;
-  const int partner = turns ? (li < hop ? lane + hop : lane - hop) : lane;
+  const NrLane l = nr_lane<V, ADJ>(a.rot, lane % LPH);
+  const bool whole = l.o2 == l.o1 + C;
   float g[V], dg[V];
+  nr_gains<T, V>(p.gain, l, g);
 #pragma unroll
-  for (int k = 0; k < V; ++k) {
-    g[k] = p.gain[li * V + k];
-    dg[k] = 0.f;
-  }
-  for (long long base = ((long long)block * WARPS + warp) * RPW; base < p.rows; base += (long long)blocks * WARPS * RPW) {
+  for (int k = 0; k < V; ++k) dg[k] = 0.f;
+  const long long step = (long long)blocks * WARPS * RPW;
+  for (long long base = ((long long)block * WARPS + warp) * RPW; base < p.rows; base += step) {
     const long long row = base + lane / LPH;
     const bool live = row < p.rows;
-    const long long r0 = live ? row : 0;
-    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const T*>(p.x) + r0 * p.ldx) + li;
+    const long long r0 = live ? row : p.rows - 1;
+    const T* x = static_cast<const T*>(p.x) + r0 * p.ldx;
     const GT* dy = static_cast<const GT*>(p.dy) + r0 * p.lddy;
     GT* dx = static_cast<GT*>(p.y) + r0 * p.ldy;
-    float c[ADJ ? V / 2 : V], s[ADJ ? V / 2 : V];
-    nr_angles<V, LPH, ADJ>(a, live ? p.pos[row] : 0, li, c, s, hop);
-#pragma unroll 2
-    for (int h = 0; h < p.heads; ++h) {
-      float f[V], d[V], e[V], dn[V];
-      const uint4 w = live ? x[h * LPH] : make_uint4(0u, 0u, 0u, 0u);
-      if (live) nr_load_grad<GT, V>(dy, h * DH + li * V, d);
-      else {
+    NrRaw<T, V> wx[HU], nx[HU];
+    NrRaw<GT, V> wd[HU], nd[HU];
 #pragma unroll
-        for (int k = 0; k < V; ++k) d[k] = 0.f;
+    for (int u = 0; u < HU; ++u)
+      if (u < p.heads) {
+        wx[u] = nr_load<T, V>(x + u * DH, l.o1, l.o2, whole);
+        wd[u] = nr_load<GT, V>(dy + u * DH, l.o1, l.o2, whole);
       }
-      NrVec<T>::unpack(w, f);
-      if constexpr (!ADJ) {
+    float c[C], s[C];
+    nr_angles<C>(a, p.pos[r0], l.first, c, s);
+    for (int h0 = 0; h0 < p.heads; h0 += HU) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) e[k] = __shfl_sync(0xffffffffu, d[k], partner);
-      }
-      nr_turn<V, ADJ, true>(d, e, c, s, dn);
-      float q = 0.f, t = 0.f;
+      for (int u = 0; u < HU; ++u)
+        if (h0 + HU + u < p.heads) {
+          nx[u] = nr_load<T, V>(x + (h0 + HU + u) * DH, l.o1, l.o2, whole);
+          nd[u] = nr_load<GT, V>(dy + (h0 + HU + u) * DH, l.o1, l.o2, whole);
+        }
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        q = fmaf(f[k], f[k], q);
-        t = fmaf(dn[k] * g[k], f[k], t);
-      }
-      const float r = rsqrtf(nr_sum<LPH>(q) * (1.0f / DH) + a.eps);
-      const float m = nr_sum<LPH>(t) * (1.0f / DH) * r * r * r;
+      for (int u = 0; u < HU; ++u) {
+        if (h0 + u < p.heads) {
+          float f[V], d[V], dn[V], e[V];
+          nr_unpack<T, V>(wx[u], f);
+          nr_unpack<GT, V>(wd[u], d);
+          float q = 0.f, t = 0.f;
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        if (live) dg[k] = fmaf(dn[k], f[k] * r, dg[k]);  // a dead lane's r is 1 / sqrt(eps): infinite at eps 0
-        e[k] = r * dn[k] * g[k] - f[k] * m;
+          for (int k = 0; k < C; ++k) {
+            constexpr auto A = nr_a<ADJ, V>;
+            constexpr auto B = nr_b<ADJ, V>;
+            dn[A(k)] = d[A(k)] * c[k] + d[B(k)] * s[k];
+            dn[B(k)] = d[B(k)] * c[k] - d[A(k)] * s[k];
+          }
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            q = fmaf(f[k], f[k], q);
+            e[k] = dn[k] * g[k];
+            t = fmaf(e[k], f[k], t);
+          }
+          const float r = rsqrtf(nr_sum<LPH>(q) * (1.0f / DH) + a.eps);
+          const float m = nr_sum<LPH>(t) * (1.0f / DH) * r * r * r;
+#pragma unroll
+          for (int k = 0; k < V; ++k) {
+            if (live) dg[k] = fmaf(dn[k], f[k] * r, dg[k]);  // a row past the end counts once
+            e[k] = r * e[k] - f[k] * m;
+          }
+          if (live) nr_store<GT, V>(dx + (h0 + u) * DH, l.o1, l.o2, whole, e);
+        }
       }
-      if (live) nr_store_grad<GT, V>(dx, h * DH + li * V, e);
+#pragma unroll
+      for (int u = 0; u < HU; ++u) {
+        wx[u] = nx[u];
+        wd[u] = nd[u];
+      }
     }
   }
 #pragma unroll
   for (int k = 0; k < V; ++k) {
 #pragma unroll
     for (int o = LPH; o < 32; o <<= 1) dg[k] += __shfl_xor_sync(0xffffffffu, dg[k], o);
-    if (lane < LPH) sums[warp][li * V + k] = dg[k];
+    if (lane < LPH) sums[warp][k < C ? l.o1 + k : l.o2 + k - C] = dg[k];
   }
   __syncthreads();
   for (int col = threadIdx.x; col < DH; col += kNrThreads) {
@@ -312,22 +334,23 @@ __global__ void __launch_bounds__(kNrThreads) norm_rotate_backward_kernel(const 
   }
 }
 
-// d_gain[part] = the sum of its blocks' partials; one block per part, DH columns x (1024 / DH) strides.
+// d_gain[part] = the sum of its blocks' partials, in fp64 (the partials are large beside what a rounding of
+// theirs may lose); one block per part, DH columns x (1024 / DH) strides.
 __global__ void __launch_bounds__(1024)
     norm_rotate_gain_kernel(const float* __restrict__ partial, int blocks0, int blocks, int dh, float* g0, float* g1) {
-  __shared__ float sums[1024];
+  __shared__ double sums[1024];
   pdl_wait();
   pdl_trigger();
   float* out = blockIdx.x ? g1 : g0;
   const int lo = blockIdx.x ? blocks0 : 0, hi = blockIdx.x ? blocks : blocks0;
   const int col = threadIdx.x % dh, k0 = threadIdx.x / dh, ks = 1024 / dh;
-  float t = 0.f;
-  for (int b = lo + k0; b < hi; b += ks) t += partial[(size_t)b * dh + col];
+  double t = 0.0;
+  for (int b = lo + k0; b < hi; b += ks) t += (double)partial[(size_t)b * dh + col];
   sums[threadIdx.x] = t;
   __syncthreads();
   if (k0 == 0 && out) {
     for (int k = 1; k < ks; ++k) t += sums[k * dh + col];
-    out[col] = t;
+    out[col] = (float)t;
   }
 }
 

@@ -2637,14 +2637,15 @@ void nr_turns(const Shape& s, const whale_rotary& r, NrArgs* a) {
 inline long long nr_blocks(const Shape& s, long long rows) {
   return cdiv<long long>(rows, kNrThreads / (s.dh / (s.bf16 ? 8 : 4)));
 }
-// The backward's blocks stay within a few per SM, so that the gains' partial sums are few.
-constexpr long long kNrBwdBlocks = 4 * kNumSM;
-inline void nr_bwd_blocks(const Shape& s, long long rows0, long long rows1, int* b0, int* b1) {
+// Blocks of the two parts: as many as there are rows for, up to `cap` in all, in proportion to the rows.
+inline void nr_split(const Shape& s, long long cap, long long rows0, long long rows1, int* b0, int* b1) {
   const long long n0 = nr_blocks(s, rows0), n1 = nr_blocks(s, rows1);
-  const long long cap = std::min(kNrBwdBlocks, n0 + n1);
+  cap = std::min(cap, n0 + n1);
   *b0 = n0 == 0 ? 0 : (int)std::max(1ll, std::min(n0, cap * n0 / (n0 + n1)));
   *b1 = n1 == 0 ? 0 : (int)std::max(1ll, std::min(n1, cap - *b0));
 }
+constexpr long long kNrFwdBlocks = 4 * kNumSM;  // resident at once: a block walks its rows with the next one's loads in flight
+constexpr long long kNrBwdBlocks = 4 * kNumSM;  // and few partial sums of the gains
 
 template <typename T, int DH>
 whale_status launch_norm_rotate(bool adj, const NrArgs& a, unsigned grid, cudaStream_t st) {
@@ -2788,9 +2789,10 @@ whale_status whale_norm_rotate(const whale_config* cfg, const whale_rotary* rota
   NrArgs a{};
   WCHECK(head_rows(s, q, nullptr, 0, &a.part[0]));
   WCHECK(head_rows(s, k, nullptr, 0, &a.part[1]));
-  const long long b0 = nr_blocks(s, a.part[0].rows), b1 = nr_blocks(s, a.part[1].rows);
+  int b0, b1;
+  nr_split(s, kNrFwdBlocks, a.part[0].rows, a.part[1].rows, &b0, &b1);
   if (b0 + b1 == 0) return WHALE_OK;
-  a.blocks0 = (int)b0;
+  a.blocks0 = b0;
   nr_turns(s, *rotary, &a);
   const bool adj = rotary->layout == WHALE_ROTATE_ADJACENT;
   const unsigned grid = (unsigned)(b0 + b1);
@@ -2832,7 +2834,7 @@ whale_status whale_norm_rotate_backward(const whale_config* cfg, const whale_rot
   if (!ws || ws_bytes < whale_norm_rotate_workspace_size(cfg, q, k) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)))
     return WHALE_ERR_WORKSPACE;
   int b0, b1;
-  nr_bwd_blocks(s, a.part[0].rows, a.part[1].rows, &b0, &b1);
+  nr_split(s, kNrBwdBlocks, a.part[0].rows, a.part[1].rows, &b0, &b1);
   a.blocks0 = b0;
   a.partial = static_cast<float*>(ws);
   nr_turns(s, *rotary, &a);
