@@ -2627,11 +2627,19 @@ whale_status head_rows(const Shape& s, const whale_head_rows* h, const whale_hea
   return WHALE_OK;
 }
 
+// The fractional part of a number of turns, times 2^64 (whole turns fall away for every position).
+unsigned long long nr_turn_fraction(long double turns) {
+  const long double f = turns - floorl(turns);
+  const long double v = f * 18446744073709551616.0L;
+  return v >= 18446744073709551615.0L ? ~0ull : (unsigned long long)v;
+}
 void nr_turns(const Shape& s, const whale_rotary& r, NrArgs* a) {
   a->rot = r.rotary_dim;
   a->eps = s.eps;
-  for (int i = 0; i < r.rotary_dim / 2; ++i)
-    a->turns[i] = std::pow(r.base, -2.0 * i / r.rotary_dim) / 6.283185307179586476925;
+  // each frequency from the one before: 64 products of 64-bit significands lose 2^-58 at most
+  const long double ratio = r.rotary_dim ? powl(r.base, -2.0L / r.rotary_dim) : 1.0L;
+  long double turns = 1.0L / 6.283185307179586476925286767L;
+  for (int i = 0; i < r.rotary_dim / 2; ++i, turns *= ratio) a->turns[i] = nr_turn_fraction(turns);
 }
 
 inline long long nr_blocks(const Shape& s, long long rows) {
@@ -2644,8 +2652,12 @@ inline void nr_split(const Shape& s, long long cap, long long rows0, long long r
   *b0 = n0 == 0 ? 0 : (int)std::max(1ll, std::min(n0, cap * n0 / (n0 + n1)));
   *b1 = n1 == 0 ? 0 : (int)std::max(1ll, std::min(n1, cap - *b0));
 }
-constexpr long long kNrFwdBlocks = 4 * kNumSM;  // resident at once: a block walks its rows with the next one's loads in flight
-constexpr long long kNrBwdBlocks = 4 * kNumSM;  // and few partial sums of the gains
+// Blocks stay resident from start to end (a block walks its rows with the next one's loads in flight), and the
+// backward's are few enough that its partial sums of the gains are.
+constexpr long long kNrFwdBlocks = kNrFwdBlocksPerSM * kNumSM;
+inline long long nr_bwd_grid(const Shape& s, int grad_dtype) {
+  return (long long)nr_backward_blocks_per_sm(s.bf16, grad_dtype == WHALE_BF16) * kNumSM;
+}
 
 template <typename T, int DH>
 whale_status launch_norm_rotate(bool adj, const NrArgs& a, unsigned grid, cudaStream_t st) {
@@ -2654,8 +2666,10 @@ whale_status launch_norm_rotate(bool adj, const NrArgs& a, unsigned grid, cudaSt
 }
 template <typename T, typename GT, int DH>
 whale_status launch_norm_rotate_backward(bool adj, const NrArgs& a, unsigned grid, cudaStream_t st) {
-  return adj ? launch_pdl(norm_rotate_backward_kernel<T, GT, DH, true>, dim3(grid), dim3(kNrThreads), 0, st, a)
-             : launch_pdl(norm_rotate_backward_kernel<T, GT, DH, false>, dim3(grid), dim3(kNrThreads), 0, st, a);
+  auto kern = adj ? norm_rotate_backward_kernel<T, GT, DH, true> : norm_rotate_backward_kernel<T, GT, DH, false>;
+  constexpr int smem = NrRing<T, GT>::SMEM;
+  CUCHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  return launch_pdl(kern, dim3(grid), dim3(kNrThreads), smem, st, a);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -2710,11 +2724,12 @@ ChunkView chunk_view(const Shape& s, const whale_cache& k, const whale_chunk& c)
   return v;
 }
 
+// One pass of a block's warps over its rows: two passes took 65 us where one takes 61 (48 histories, d 256, e4m3).
 template <int DH, bool FP8>
-whale_status launch_rows(bool append, const RowsArgs& a, cudaStream_t st) {
-  const long long grid = cdiv<long long>(a.c.total, kRowsThreads / (DH / 8));
-  return launch_pdl(append ? cache_append_kernel<DH, FP8> : cache_read_kernel<DH, FP8>, dim3((unsigned)grid),
-                    dim3(kRowsThreads), 0, st, a);
+whale_status launch_rows(bool append, RowsArgs a, cudaStream_t st) {
+  a.rows_per_block = kRowsThreads / (DH / 8);
+  return launch_pdl(append ? cache_append_kernel<DH, FP8> : cache_read_kernel<DH, FP8>,
+                    dim3((unsigned)cdiv<long long>(a.c.total, a.rows_per_block)), dim3(kRowsThreads), 0, st, a);
 }
 
 // Row blocks and workspace of the attention over the cache.
@@ -2812,7 +2827,7 @@ whale_status whale_norm_rotate(const whale_config* cfg, const whale_rotary* rota
 size_t whale_norm_rotate_workspace_size(const whale_config* cfg, const whale_head_rows* q, const whale_head_rows* k) {
   Shape s;
   if (validate(cfg, &s) != WHALE_OK || (q && q->rows < 0) || (k && k->rows < 0)) return 0;
-  return align_up((size_t)(kNrBwdBlocks + 2) * s.dh * 4);
+  return align_up((size_t)(4 * kNumSM) * s.dh * 4);
 }
 
 whale_status whale_norm_rotate_backward(const whale_config* cfg, const whale_rotary* rotary, const whale_head_rows* q,
@@ -2834,7 +2849,7 @@ whale_status whale_norm_rotate_backward(const whale_config* cfg, const whale_rot
   if (!ws || ws_bytes < whale_norm_rotate_workspace_size(cfg, q, k) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)))
     return WHALE_ERR_WORKSPACE;
   int b0, b1;
-  nr_split(s, kNrBwdBlocks, a.part[0].rows, a.part[1].rows, &b0, &b1);
+  nr_split(s, nr_bwd_grid(s, grad_dtype), a.part[0].rows, a.part[1].rows, &b0, &b1);
   a.blocks0 = b0;
   a.partial = static_cast<float*>(ws);
   nr_turns(s, *rotary, &a);
