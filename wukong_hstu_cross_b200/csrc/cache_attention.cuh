@@ -569,74 +569,4 @@ __global__ void __launch_bounds__(kCaThreads, 1) cache_attend_kernel(const Cache
   }
 }
 
-// One CTA per (sequence, K|V head, row block): joins the partials of the item, if it was cut.
-constexpr int kCaMergeThreads = 256;
-template <int DH, int BM>
-__global__ void __launch_bounds__(kCaMergeThreads) cache_attend_merge_kernel(const CacheAttnArgs p, int warps) {
-  __shared__ float4 so[kCaMergeThreads];
-  __shared__ float2 sml[kCaMergeThreads];
-  pdl_wait();
-  pdl_trigger();
-  const int qb = blockIdx.x % p.n_qb, kvh = blockIdx.x / p.n_qb % p.c.kv_heads, b = blockIdx.x / (p.n_qb * p.c.kv_heads);
-  const CaSeq s = ca_seq(p, b, BM);
-  if (qb >= s.blocks) return;
-  const long long T = p.before[p.c.B], W = ca_workers(T, warps);
-  const long long u0 = p.before[b] + (long long)(kvh * s.blocks + qb) * s.units, u1 = u0 + s.units - 1;
-  const long long w0 = ((u0 + 1) * W - 1) / T, w1 = ((u1 + 1) * W - 1) / T;
-  if (w0 == w1) return;
-  const int n_rows = min(BM, s.take * p.group - qb * BM), n = (int)(w1 - w0 + 1);
-  const int vecs = n_rows * (DH / 4);
-  // `groups` threads take every groups-th partial of one vector of 4 columns
-  int groups = 1;
-  while (groups * 2 * vecs <= kCaMergeThreads && groups < n) groups *= 2;
-  const int per = kCaMergeThreads / groups, grp = threadIdx.x / per;
-  for (int v0 = 0; v0 < vecs; v0 += per) {
-    const int v = v0 + threadIdx.x % per;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int r = v / (DH / 4), c4 = v % (DH / 4);
-    if (v < vecs) {
-#pragma unroll 4
-      for (int k = grp; k < n; k += groups) {
-        const long long w = w0 + k;
-        const long long slot = (2 * w + (w * T / W < u0 ? 1 : 0)) * BM + r;
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot * 2);
-        const float4 x = *reinterpret_cast<const float4*>(p.part_o + slot * DH + 4 * c4);
-        const float mn = fmaxf(m, ml.x);
-        const float fo = m == mn ? 1.f : fast_exp2(m - mn), fx = ml.x == mn ? 1.f : fast_exp2(ml.x - mn);
-        m = mn;
-        l = l * fo + ml.y * fx;
-        o.x = o.x * fo + x.x * fx;
-        o.y = o.y * fo + x.y * fx;
-        o.z = o.z * fo + x.z * fx;
-        o.w = o.w * fo + x.w * fx;
-      }
-    }
-    if (groups > 1) {  // one round: vecs <= per
-      so[threadIdx.x] = o;
-      sml[threadIdx.x] = make_float2(m, l);
-      __syncthreads();
-      if (grp == 0 && v < vecs)
-        for (int k = 1; k < groups; ++k) {
-          const float2 ml = sml[k * per + v];
-          const float4 x = so[k * per + v];
-          const float mn = fmaxf(m, ml.x);
-          const float fo = m == mn ? 1.f : fast_exp2(m - mn), fx = ml.x == mn ? 1.f : fast_exp2(ml.x - mn);
-          m = mn;
-          l = l * fo + ml.y * fx;
-          o.x = o.x * fo + x.x * fx;
-          o.y = o.y * fo + x.y * fx;
-          o.z = o.z * fo + x.z * fx;
-          o.w = o.w * fo + x.w * fx;
-        }
-    }
-    if (grp == 0 && v < vecs) {
-      const float f = l == 0.f ? 0.f : 1.f / l;
-      const int row = qb * BM + r, tok = row / p.group, head = kvh * p.group + row % p.group;
-      *reinterpret_cast<uint2*>(p.a + (long long)(s.first_row + tok) * p.lda + head * DH + 4 * c4) =
-          make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
-    }
-  }
-}
-
 }  // namespace whale

@@ -1,0 +1,664 @@
+// cache_attention_tc.cuh — attention of a chunk over the paged cache, many rows per sequence (chunks of new events,
+// candidates' tokens): the products on tcgen05, the softmax between them in registers. The formula, the row order
+// and the masks are those of cache_attention.cuh.
+//
+// Bound: the exponentials. A tile of 128 rows x 128 positions takes 16384 of them, 1024 cycles of the SM's
+// special-function units (16 a cycle), beside 2 * 128 * 128 * d_head multiply-adds in 128 (d_head 32) or 256 cycles
+// each. Three of every eight are therefore formed on the FMA pipe (cp_exp2), which leaves 640 cycles of either.
+//
+// One CTA per SM takes a contiguous slice of the units (128 positions of one item = (sequence, K|V head, block of 256
+// rows)), all items' units laid end to end; causal items end at their last row's position. Partials where a slice cuts an
+// item, joined by cache_attend_merge_kernel in the order of the slices. Inside a CTA, for two tiles of 128 rows:
+//   warps 0-1   queries, and K and V of a unit, into 3 stages: bf16 by cp.async, e4m3 through registers, where
+//               number * 2^e becomes the bf16 number that it is. Rows in no page or past the end are zeros.
+//   warp 2      S = Q K^T (128 x 128, K = d_head) and O += P V (128 x d_head, K = 128) as their operands come
+//   warps 3-10  one thread per row: scores out of tensor memory, running maximum (the reference is raised when the
+//               tile's maximum exceeds it by 2^8, with the rescale of O in tensor memory then), weights to
+//               shared memory as bf16, sums in fp32; at an item's end O / l, or the partial.
+#pragma once
+
+#include "cache_attention.cuh"
+
+namespace whale {
+
+constexpr int kCpRows = 256;     // rows of an item: two tiles
+constexpr int kCpUnit = 128;     // positions of a unit
+constexpr int kCpThreads = 352;
+constexpr int kCpProducers = 64;
+constexpr int kCpMinUnits = 2;
+
+template <int DH>
+struct CpSmem {
+  static constexpr int ROW = 2 * DH;                         // bytes of a row of Q, K, V
+  static constexpr uint32_t TILE = 128 * ROW;                // 128 rows
+  static constexpr int ST = 3;
+  static constexpr uint32_t P_TILE = 128 * 128 * 2;          // two blocks of 64 positions
+  static constexpr int OFF_Q = 0;                            // [2 buffers][2 tiles]
+  static constexpr int OFF_KV = OFF_Q + 4 * (int)TILE;       // [ST][K, V]
+  static constexpr int OFF_P = OFF_KV + ST * 2 * (int)TILE;  // [2 tiles]
+  static constexpr int OFF_BAR = OFF_P + 2 * (int)P_TILE;
+  // kvfull[ST], kvempty[ST], qfree[2], sfull[2], sfree[2], pfull[2], pfree[2], tmem slot, abort flag
+  static constexpr size_t BYTES = 1024 + OFF_BAR + (2 * ST + 10) * 8 + 16;
+  static_assert(BYTES <= 232448 - 1024, "shared memory of one CTA");
+  // byte offset of 16-byte chunk ch of row r: the 128-byte (d_head 64) or 64-byte swizzle
+  static __device__ __forceinline__ uint32_t at(int r, int ch) {
+    return (uint32_t)r * ROW + (uint32_t)((ch ^ (DH == 64 ? r & 7 : (r >> 1) & 3)) << 4);
+  }
+  // matrix descriptors of rows of ROW bytes: K-major (Q, K), MN-major (V)
+  static __device__ __forceinline__ uint64_t desc(uint32_t saddr) {
+    uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu) | (uint64_t)1u << 16 | (uint64_t)1u << 46;
+    d |= (uint64_t)((8 * ROW) >> 4) << 32;                   // 8-row groups
+    d |= (uint64_t)(DH == 64 ? 2u : 4u) << 61;
+    return d;
+  }
+};
+
+// Units of one (K|V head, row block) of a sequence, and of all its row blocks.
+__device__ __forceinline__ int cp_units(const CacheAttnArgs& p, const CaSeq& s, long long pos0, int qb) {
+  long long e = s.len;
+  if (p.causal) {
+    const int last = (min(s.take * p.group, (qb + 1) * kCpRows) - 1) / p.group;
+    e = min(e, pos0 + last + 1);
+  }
+  return e <= kCpUnit ? 1 : (int)((e + kCpUnit - 1) / kCpUnit);
+}
+__device__ __forceinline__ long long cp_head_units(const CacheAttnArgs& p, const CaSeq& s, int b, int blocks) {
+  if (!p.causal) return blocks ? (long long)blocks * cp_units(p, s, 0, 0) : 0;
+  const long long pos0 = (long long)p.c.lengths[b] - s.rows;
+  long long n = 0;
+  for (int qb = 0; qb < blocks; ++qb) n += cp_units(p, s, pos0, qb);
+  return n;
+}
+__device__ __forceinline__ long long cp_workers(long long T, long long W) {
+  const long long w = (T + kCpMinUnits - 1) / kCpMinUnits;
+  return w < W ? w : W;
+}
+
+// A CTA's slice, segment by segment; every role walks it for itself.
+struct CpWalk {
+  long long u, u_lo, u_hi, at, head_units;
+  int b;
+  CaSeq s;
+  // the segment
+  long long pos0;
+  int kvh, qb, t_lo, t_hi, units, n_rows;
+
+  __device__ __forceinline__ void sequence(const CacheAttnArgs& p, int b_) {
+    b = b_;
+    s = ca_seq(p, b, kCpRows);
+    head_units = cp_head_units(p, s, b, s.blocks);
+    pos0 = (long long)p.c.lengths[b] - s.rows;
+  }
+  __device__ __forceinline__ bool next(const CacheAttnArgs& p) {
+    if (u >= u_hi) return false;
+    while (u >= at + head_units * p.c.kv_heads) {
+      if (b + 1 >= p.c.B) return false;
+      at += head_units * p.c.kv_heads;
+      sequence(p, b + 1);
+    }
+    kvh = (int)((u - at) / head_units);
+    long long rem = (u - at) - kvh * head_units;
+    if (!p.causal) {
+      units = cp_units(p, s, pos0, 0);
+      qb = (int)(rem / units);
+      rem -= (long long)qb * units;
+    } else {
+      for (qb = 0; rem >= (units = cp_units(p, s, pos0, qb)); ++qb) rem -= units;
+    }
+    t_lo = (int)rem;
+    t_hi = (int)min((long long)units, t_lo + (u_hi - u));
+    n_rows = min(kCpRows, s.take * p.group - qb * kCpRows);
+    return true;
+  }
+  __device__ __forceinline__ void done() { u += t_hi - t_lo; }
+};
+
+// 2^x of two numbers on the FMA pipe, x <= 8: n = round(x) by the 1.5 * 2^23 trick, 2^(x - n) by the cubic of
+// exp2_fma (relative error 7.5e-5, below the weights' rounding to bf16), n added to the exponent. Below -125: 2^-125.
+__device__ __forceinline__ void cp_exp2(uint64_t x, float& y0, float& y1) {
+  float x0, x1, t0, t1, p0, p1;
+  f2unpack(x, x0, x1);
+  asm("max.NaN.f32 %0, %0, 0fC2FA0000;" : "+f"(x0));  // -125; a NaN shows in the result
+  asm("max.NaN.f32 %0, %0, 0fC2FA0000;" : "+f"(x1));
+  const uint64_t xc = f2pack(x0, x1);
+  const uint64_t big = f2pack(12582912.0f, 12582912.0f);
+  const uint64_t t = fadd2(xc, big);
+  const uint64_t n = fadd2(t, f2pack(-12582912.0f, -12582912.0f));
+  const uint64_t f = ffma2(n, f2pack(-1.0f, -1.0f), xc);
+  uint64_t q = ffma2(f2pack(0.05517113208770752f, 0.05517113208770752f), f, f2pack(0.24261008203029633f, 0.24261008203029633f));
+  q = ffma2(q, f, f2pack(0.6932609677314758f, 0.6932609677314758f));
+  q = ffma2(q, f, f2pack(0.9999281167984009f, 0.9999281167984009f));
+  f2unpack(t, t0, t1);
+  f2unpack(q, p0, p1);
+  y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
+  y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
+}
+
+// Eight e4m3 numbers times 2^e as bf16 (exact).
+__device__ __forceinline__ uint4 cp_bf16x8(uint2 q, float f) {
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = e4m3x2_f16x2((uint16_t)((i < 2 ? q.x : q.y) >> (16 * (i & 1))));
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v));
+    o[i] = pack_bf16x2(x.x * f, x.y * f);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+template <int DH, bool FP8>
+__global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __grid_constant__ CacheAttnArgs p) {
+  using L = CpSmem<DH>;
+  constexpr int ST = L::ST;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long sums[kCpThreads / 32 + 1];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* kvfull = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  uint64_t* kvempty = kvfull + ST;
+  uint64_t* qfree = kvempty + ST;  // [2] queries of a segment read by its last S
+  uint64_t* sfull = qfree + 2;     // [2] per tile, as in attention_qtile.cuh
+  uint64_t* sfree = sfull + 2;
+  uint64_t* pfull = sfree + 2;
+  uint64_t* pfree = pfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pfree + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int s = 0; s < ST; ++s) {
+      mbar_init(&kvfull[s], kCpProducers / 32);
+      mbar_init(&kvempty[s], 1);
+    }
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&qfree[h], 1);
+      mbar_init(&sfull[h], 1);
+      mbar_init(&sfree[h], 4);
+      mbar_init(&pfull[h], 4);
+      mbar_init(&pfree[h], 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 2) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // units before each thread's run of sequences; the slice; its first sequence
+  __shared__ int start_b;
+  __shared__ long long start_at;
+  const int run = (p.c.B + kCpThreads - 1) / kCpThreads;
+  const int b_lo = min(p.c.B, tid * run), b_hi = min(p.c.B, b_lo + run);
+  auto seq_units = [&](int b) {
+    const CaSeq s = ca_seq(p, b, kCpRows);
+    return cp_head_units(p, s, b, s.blocks) * p.c.kv_heads;
+  };
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += seq_units(b);
+  long long scan = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) sums[warp] = scan;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  long long base = 0, T = 0;
+  for (int w = 0; w < kCpThreads / 32; ++w) {
+    base += w < warp ? sums[w] : 0;
+    T += sums[w];
+  }
+  const long long W = cp_workers(T, gridDim.x);
+  CpWalk walk;
+  walk.u_lo = walk.u = W > (long long)blockIdx.x ? (long long)blockIdx.x * T / W : T;
+  walk.u_hi = W > (long long)blockIdx.x ? ((long long)blockIdx.x + 1) * T / W : T;
+  {
+    long long at = base + scan - mine;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const long long n = seq_units(b);
+      if (blockIdx.x == 0) p.before[b] = at;
+      if (at <= walk.u_lo && walk.u_lo < at + n) {
+        start_b = b;
+        start_at = at;
+      }
+      at += n;
+    }
+    if (blockIdx.x == 0 && tid == kCpThreads - 1) p.before[p.c.B] = T;
+  }
+  __syncthreads();
+  if (walk.u < walk.u_hi) {
+    walk.at = start_at;
+    walk.sequence(p, start_b);
+  }
+
+  if (warp < 2) {
+    // ---------------- producers ----------------
+    constexpr int CH = L::ROW / 16, RPI = 32 / CH;  // 16-byte chunks of a row, rows of a warp's instruction
+    int n = 0, seg = 0;                             // tiles and segments so far
+    bool ok = true;
+    const long long v_off = p.c.planes == 2 ? (long long)p.c.kv_heads << p.c.page_shift : 0;
+    for (; ok && walk.next(p); walk.done(), ++seg) {
+      const long long kv_off = (long long)walk.kvh << p.c.page_shift;
+      if (tid == 0 && p.c.lengths[walk.b] > walk.s.len) atomicOr(&g_device_error, kErrPages);
+      if (tid == 0 && walk.s.rows > walk.s.take) atomicOr(&g_device_error, kErrOffsets);
+      // rows (of each plane's first head) of this lane's two positions of unit i: the warp has 64 of the 128
+      long long at[2];
+      auto look = [&](int i) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int pos = i * kCpUnit + warp * 64 + k * 32 + lane;
+          at[k] = -1;
+          if (i < walk.t_hi && pos < walk.s.len) {
+            const long long r = cache_row(p.c, walk.b, pos);
+            if (r < 0) atomicOr(&g_device_error, kErrPages);
+            else at[k] = r + kv_off;
+          }
+        }
+      };
+      look(walk.t_lo);
+      // queries into this segment's buffer
+      if (seg >= 2 && !mbar_wait(&qfree[seg & 1], ((seg >> 1) - 1) & 1, abort_flag)) break;
+      const uint32_t q_base = smem_u32(smem + L::OFF_Q) + (seg & 1) * 2 * L::TILE;
+#pragma unroll 4
+      for (int k = 0; k < kCpRows / 2 / RPI; ++k) {
+        const int r = warp * (kCpRows / 2) + k * RPI + lane / CH, ch = lane % CH;
+        const bool live = r < walk.n_rows;
+        const int row = walk.qb * kCpRows + (live ? r : 0), tok = row / p.group, head = walk.kvh * p.group + row % p.group;
+        cp_async16(q_base + (r >> 7) * L::TILE + L::at(r & 127, ch),
+                   p.q + (long long)(walk.s.first_row + tok) * p.ldq + head * DH + ch * 8, live ? 16u : 0u);
+      }
+      if constexpr (!FP8) {
+        for (int i = walk.t_lo; i < walk.t_hi; ++i, ++n) {
+          if (n >= ST && !mbar_wait(&kvempty[n % ST], (n / ST - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = smem_u32(smem + L::OFF_KV) + (n % ST) * 2 * L::TILE;
+          const long long a0 = at[0], a1 = at[1];
+          look(i + 1);
+#pragma unroll
+          for (int k = 0; k < 64 / RPI; ++k) {
+            const int r = k * RPI + lane / CH, ch = lane % CH;
+            const long long src = __shfl_sync(0xffffffffu, k * RPI < 32 ? a0 : a1, r & 31);
+            const uint8_t* a = p.pages + (src < 0 ? 0 : src) * L::ROW + ch * 16;
+            const uint32_t dst = st + L::at(warp * 64 + r, ch), bytes = src < 0 ? 0u : 16u;
+            cp_async16(dst, a, bytes);
+            cp_async16(dst + L::TILE, a + (src < 0 ? 0 : v_off * L::ROW), bytes);
+          }
+          cp_async_commit();
+          if (i > walk.t_lo) {  // the tile before has arrived: hand it to the MMA
+            cp_async_wait<1>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kvfull[(n - 1) % ST]);
+          }
+        }
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&kvfull[(n - 1) % ST]);
+      } else {
+        constexpr int RCH = DH / 16, RRPI = 32 / RCH, PASS = 64 / RRPI;  // raw rows are DH bytes
+        uint4 raw[2][PASS];
+        uint32_t sc[2][PASS];
+        auto load = [&]() {
+#pragma unroll
+          for (int k = 0; k < PASS; ++k) {
+            const int r = k * RRPI + lane / RCH, ch = lane % RCH;
+            const long long src = __shfl_sync(0xffffffffu, k * RRPI < 32 ? at[0] : at[1], r & 31);
+#pragma unroll
+            for (int pl = 0; pl < 2; ++pl) {
+              raw[pl][k] = make_uint4(0u, 0u, 0u, 0u);
+              sc[pl][k] = 0u;
+              if (src >= 0) {
+                const long long row = src + pl * v_off;
+                raw[pl][k] = *reinterpret_cast<const uint4*>(p.pages + row * DH + ch * 16);
+                sc[pl][k] = p.scales[row];
+              }
+            }
+          }
+        };
+        load();
+        for (int i = walk.t_lo; i < walk.t_hi; ++i, ++n) {
+          look(i + 1);
+          if (n >= ST && !mbar_wait(&kvempty[n % ST], (n / ST - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t st = smem_u32(smem + L::OFF_KV) + (n % ST) * 2 * L::TILE;
+#pragma unroll
+          for (int k = 0; k < PASS; ++k) {
+            const int r = warp * 64 + k * RRPI + lane / RCH, ch = lane % RCH;
+#pragma unroll
+            for (int pl = 0; pl < 2; ++pl) {
+              const float f = __uint_as_float(sc[pl][k] << 23);
+              sts128(st + pl * L::TILE + L::at(r, 2 * ch), cp_bf16x8(make_uint2(raw[pl][k].x, raw[pl][k].y), f));
+              sts128(st + pl * L::TILE + L::at(r, 2 * ch + 1), cp_bf16x8(make_uint2(raw[pl][k].z, raw[pl][k].w), f));
+            }
+          }
+          if (i + 1 < walk.t_hi) load();
+          if (i == walk.t_lo) {  // the queries too
+            cp_async_commit();
+            cp_async_wait<0>();
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&kvfull[n % ST]);
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else if (warp == 2) {
+    // ---------------- MMA issuer ----------------
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DH) | kIdescBMnMajor;
+      const uint32_t kv0 = smem_u32(smem + L::OFF_KV), q0 = smem_u32(smem + L::OFF_Q), p0 = smem_u32(smem + L::OFF_P);
+      int n = 0, seg = 0;         // tiles and segments so far
+      int c[2] = {0, 0};          // blocks of each tile so far (its barriers' phases)
+      bool ok = true;
+      for (; ok && walk.next(p); walk.done(), ++seg) {
+        const int blocks = walk.t_hi - walk.t_lo, tiles = walk.n_rows > 128 ? 2 : 1;
+        int si[2] = {0, tiles == 2 ? 0 : blocks}, pi[2] = {0, tiles == 2 ? 0 : blocks};  // next S, next P V of a tile
+        int freed = 0;
+        bool q_given = false;
+        uint64_t idle = 0;
+        while (freed < blocks) {
+          bool did = false;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (si[h] < blocks && si[h] <= pi[h] + 1) {
+              const int i = n + si[h];
+              if ((c[h] + si[h] == 0 || mbar_test(&sfree[h], (c[h] + si[h] - 1) & 1)) &&
+                  mbar_test(&kvfull[i % ST], (i / ST) & 1)) {
+                tc_fence_after();
+                const uint32_t k_base = kv0 + (i % ST) * 2 * L::TILE, q_base = q0 + ((seg & 1) * 2 + h) * L::TILE;
+#pragma unroll
+                for (int k = 0; k < DH / 16; ++k)
+                  umma_f16(tmem_base + h * 128, L::desc(q_base + k * 32), L::desc(k_base + k * 32), idesc_s, k > 0 ? 1u : 0u);
+                umma_commit(&sfull[h]);
+                ++si[h];
+                did = true;
+              }
+            }
+            if (pi[h] < si[h] && pi[h] < blocks && mbar_test(&pfull[h], (c[h] + pi[h]) & 1)) {
+              tc_fence_after();
+              const int i = n + pi[h];
+              const uint32_t v_base = kv0 + ((i % ST) * 2 + 1) * L::TILE, p_base = p0 + h * L::P_TILE;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                umma_f16(tmem_base + 256 + h * 64, sdesc_k_sw128(p_base + (k >> 2) * 16384 + (k & 3) * 32),
+                         L::desc(v_base + k * 16 * L::ROW), idesc_pv, (pi[h] > 0 || k > 0) ? 1u : 0u);
+              umma_commit(&pfree[h]);
+              ++pi[h];
+              did = true;
+            }
+          }
+          if (!q_given && si[0] == blocks && si[1] == blocks) {
+            umma_commit(&qfree[seg & 1]);
+            q_given = true;
+          }
+          if (min(pi[0], pi[1]) > freed) {
+            umma_commit(&kvempty[(n + freed) % ST]);
+            ++freed;
+          }
+          if (did) {
+            idle = 0;
+          } else {
+            if (*abort_flag) {
+              ok = false;
+              break;
+            }
+            const uint64_t now = globaltimer_ns();
+            if (idle == 0) idle = now;
+            else if (now - idle > kWaitLimitNs) {
+              atomicOr(&g_device_error, kErrTimeout);
+              *abort_flag = 1;
+              ok = false;
+              break;
+            }
+          }
+        }
+        n += blocks;
+        c[0] += blocks;
+        if (tiles == 2) c[1] += blocks;
+      }
+    }
+  } else {
+    // ---------------- softmax and output: one thread per row ----------------
+    const int q4 = warp & 3, h = (warp - 3) >> 2, row = q4 * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+    const uint32_t s_tm = tmem_base + h * 128 + lane_off, o_tm = tmem_base + 256 + h * 64 + lane_off;
+    const uint32_t p_row = smem_u32(smem + L::OFF_P) + h * L::P_TILE + row * 128;
+    int c = 0;  // blocks of this tile so far
+    bool ok = true;
+    for (; ok && walk.next(p); walk.done()) {
+      if (walk.n_rows <= 128 * h) continue;
+      const int blocks = walk.t_hi - walk.t_lo;
+      const int r = 128 * h + row;
+      const bool live = r < walk.n_rows;
+      const int srow = walk.qb * kCpRows + (live ? r : 0), tok = srow / p.group;
+      int end = walk.s.len;
+      if (p.causal) end = (int)max(0ll, min((long long)end, walk.pos0 + tok + 1));
+      float m_run = -INFINITY, l = 0.f;
+      for (int i = 0; i < blocks && ok; ++i, ++c) {
+        if (!mbar_wait(&sfull[h], c & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t v[128];
+        tmem_ld_32x32b_x32(s_tm + 0, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+        tmem_ld_32x32b_x32(s_tm + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+        tmem_ld_32x32b_x32(s_tm + 64, *reinterpret_cast<uint32_t(*)[32]>(&v[64]));
+        tmem_ld_32x32b_x32(s_tm + 96, *reinterpret_cast<uint32_t(*)[32]>(&v[96]));
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sfree[h]);
+        const int nv = end - (walk.t_lo + i) * kCpUnit;  // positions of the block that this row sees
+        const bool full = __all_sync(0xffffffffu, nv >= kCpUnit);
+        if (!full) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (j >= nv) v[j] = __float_as_uint(-INFINITY);
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 128; j += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx[k] = fmax3(mx[k], __uint_as_float(v[j + 2 * k]), __uint_as_float(v[j + 2 * k + 1]));
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        const float m_new = mt > m_run + kCaLazy ? mt : m_run;
+        // P of the block before has been read and O updated: P may be rewritten, O rescaled
+        if (i > 0 && !mbar_wait(&pfree[h], (c - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (i > 0 && __any_sync(0xffffffffu, m_new != m_run)) {
+          tc_fence_after();
+          const float f = m_new == m_run ? 1.f : fast_exp2(m_run - m_new);
+#pragma unroll 1
+          for (int k = 0; k < DH / 32; ++k) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(o_tm + k * 32, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+            tmem_st_32x32b_x32(o_tm + k * 32, o);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          l *= f;
+        }
+        m_run = m_new;
+        const float ref = m_run == -INFINITY ? 0.f : m_run;
+        const uint64_t sc2 = f2pack(p.scale_log2, p.scale_log2), nr2 = f2pack(-ref, -ref);
+        auto exp_pass = [&](auto full_tag) {
+          constexpr bool kFull = decltype(full_tag)::value;
+          uint64_t ls[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
+#pragma unroll
+          for (int ch = 0; ch < 16; ++ch) {  // 16 chunks of 8 positions
+            uint32_t pk[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint64_t x = ffma2(f2pack(__uint_as_float(v[8 * ch + 2 * k]), __uint_as_float(v[8 * ch + 2 * k + 1])), sc2, nr2);
+              float w0, w1;
+              if (kFull && (ch % 8 == 1 || ch % 8 == 4 || ch % 8 == 6)) {
+                cp_exp2(x, w0, w1);
+              } else {
+                f2unpack(x, w0, w1);
+                w0 = fast_exp2(w0);
+                w1 = fast_exp2(w1);
+              }
+              ls[k & 1] = fadd2(ls[k & 1], f2pack(w0, w1));
+              pk[k] = pack_bf16x2(w0, w1);
+            }
+            sts128(p_row + (ch >> 3) * 16384 + (((ch & 7) ^ (row & 7)) << 4), make_uint4(pk[0], pk[1], pk[2], pk[3]));
+          }
+          float a0, a1;
+          f2unpack(fadd2(ls[0], ls[1]), a0, a1);
+          l += a0 + a1;
+        };
+        if (full) exp_pass(std::true_type{});
+        else exp_pass(std::false_type{});
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&pfull[h]);
+      }
+      if (!ok || !mbar_wait(&pfree[h], (c - 1) & 1, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool whole = walk.t_lo == 0 && walk.t_hi == walk.units;
+      const long long slot = 2 * (long long)blockIdx.x + (walk.u != walk.u_lo);
+      const float f = whole ? (l == 0.f ? 0.f : 1.0f / l) : 1.f;
+      const int head = walk.kvh * p.group + srow % p.group;
+      __nv_bfloat16* dst = p.a + (long long)(walk.s.first_row + tok) * p.lda + head * DH;
+      float* po = p.part_o + (slot * kCpRows + r) * DH;
+#pragma unroll 1
+      for (int k = 0; k < DH / 32; ++k) {  // collective: every lane loads, live rows are stored
+        uint32_t o[32];
+        tmem_ld_32x32b_x32(o_tm + k * 32, o);
+        tmem_ld_wait();
+        if (!live) continue;
+        if (whole) {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(__uint_as_float(o[2 * j]) * f, __uint_as_float(o[2 * j + 1]) * f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(dst + k * 32 + 8 * j) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(po + k * 32 + 4 * j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        }
+      }
+      if (live && !whole) *reinterpret_cast<float2*>(p.part_ml + (slot * kCpRows + r) * 2) = make_float2(m_run, l);
+      tc_fence_before();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// One CTA per (sequence, K|V head, row block) and kCaMergeRows of its rows: joins the partials of the item, if it was
+// cut, in the order of the slices. TC: those of cache_attend_tc_kernel (blocks of 256 rows), else cache_attend_kernel's.
+constexpr int kCaMergeThreads = 256, kCaMergeRows = 32;
+template <int DH, int BM, bool TC>
+__global__ void __launch_bounds__(kCaMergeThreads) cache_attend_merge_kernel(const CacheAttnArgs p, int workers) {
+  __shared__ float4 so[kCaMergeThreads];
+  __shared__ float2 sml[kCaMergeThreads];
+  pdl_wait();
+  pdl_trigger();
+  const int qb = blockIdx.x % p.n_qb, kvh = blockIdx.x / p.n_qb % p.c.kv_heads, b = blockIdx.x / (p.n_qb * p.c.kv_heads);
+  const CaSeq s = ca_seq(p, b, BM);
+  if (qb >= s.blocks) return;
+  const int row0 = blockIdx.y * kCaMergeRows;  // first row in the block
+  const int n_rows = min(kCaMergeRows, min(BM, s.take * p.group - qb * BM) - row0);
+  if (n_rows <= 0) return;
+  const long long T = p.before[p.c.B], W = TC ? cp_workers(T, workers) : ca_workers(T, workers);
+  long long u0 = p.before[b], units = s.units;
+  if constexpr (TC) {
+    const long long pos0 = (long long)p.c.lengths[b] - s.rows;
+    units = cp_units(p, s, pos0, qb);
+    u0 += kvh * cp_head_units(p, s, b, s.blocks) + cp_head_units(p, s, b, qb);
+  } else {
+    u0 += (long long)(kvh * s.blocks + qb) * units;
+  }
+  const long long u1 = u0 + units - 1;
+  const long long w0 = ((u0 + 1) * W - 1) / T, w1 = ((u1 + 1) * W - 1) / T;
+  if (w0 == w1) return;
+  const int n = (int)(w1 - w0 + 1);
+  const int vecs = n_rows * (DH / 4);
+  // `groups` threads take every groups-th partial of one vector of 4 columns
+  int groups = 1;
+  while (groups * 2 * vecs <= kCaMergeThreads && groups < n) groups *= 2;
+  const int per = kCaMergeThreads / groups, grp = threadIdx.x / per;
+  for (int v0 = 0; v0 < vecs; v0 += per) {
+    const int v = v0 + threadIdx.x % per;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int r = v / (DH / 4), c4 = v % (DH / 4);
+    if (v < vecs) {
+#pragma unroll 4
+      for (int k = grp; k < n; k += groups) {
+        const long long w = w0 + k;
+        const long long slot = (2 * w + (w * T / W < u0 ? 1 : 0)) * BM + row0 + r;
+        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot * 2);
+        const float4 x = *reinterpret_cast<const float4*>(p.part_o + slot * DH + 4 * c4);
+        const float mn = fmaxf(m, ml.x);
+        const float fo = m == mn ? 1.f : fast_exp2(m - mn), fx = ml.x == mn ? 1.f : fast_exp2(ml.x - mn);
+        m = mn;
+        l = l * fo + ml.y * fx;
+        o.x = o.x * fo + x.x * fx;
+        o.y = o.y * fo + x.y * fx;
+        o.z = o.z * fo + x.z * fx;
+        o.w = o.w * fo + x.w * fx;
+      }
+    }
+    if (groups > 1) {  // one round: vecs <= per
+      so[threadIdx.x] = o;
+      sml[threadIdx.x] = make_float2(m, l);
+      __syncthreads();
+      if (grp == 0 && v < vecs)
+        for (int k = 1; k < groups; ++k) {
+          const float2 ml = sml[k * per + v];
+          const float4 x = so[k * per + v];
+          const float mn = fmaxf(m, ml.x);
+          const float fo = m == mn ? 1.f : fast_exp2(m - mn), fx = ml.x == mn ? 1.f : fast_exp2(ml.x - mn);
+          m = mn;
+          l = l * fo + ml.y * fx;
+          o.x = o.x * fo + x.x * fx;
+          o.y = o.y * fo + x.y * fx;
+          o.z = o.z * fo + x.z * fx;
+          o.w = o.w * fo + x.w * fx;
+        }
+    }
+    if (grp == 0 && v < vecs) {
+      const float f = l == 0.f ? 0.f : 1.f / l;
+      const int row = qb * BM + row0 + r, tok = row / p.group, head = kvh * p.group + row % p.group;
+      *reinterpret_cast<uint2*>(p.a + (long long)(s.first_row + tok) * p.lda + head * DH + 4 * c4) =
+          make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+    }
+  }
+}
+
+}  // namespace whale

@@ -36,6 +36,7 @@
 #include "attention_bwd_tc.cuh"
 #include "backward.cuh"
 #include "cache_attention.cuh"
+#include "cache_attention_tc.cuh"
 #include "fp32_path.cuh"
 #include "gemm_2sm.cuh"
 #include "gemm_tc.cuh"
@@ -2741,12 +2742,12 @@ whale_status plan_cache_attention(const Shape& s, const whale_cache& k, const wh
   const int group = s.h / k.n_kv_heads;
   p->max_new = (int)std::min<long long>(c.max_new, c.total_new);
   const long long rows = (long long)p->max_new * group;
-  p->bm = rows <= 16 ? 16 : 32;
+  p->bm = rows <= 16 ? 16 : (rows <= 32 ? 32 : kCpRows);
   // rows and positions are counted in 32 bits in the kernels
   if (c.total_new * s.h >= (1ll << 31) || c.max_length > (1 << 30)) return WHALE_ERR_UNSUPPORTED;
   p->n_qb = (int)std::max(1ll, cdiv<long long>(rows, p->bm));
   if ((double)c.B * k.n_kv_heads * p->n_qb >= 2147483647.0) return WHALE_ERR_UNSUPPORTED;
-  const size_t slots = 2 * (size_t)kNumSM * kCaWarps;
+  const size_t slots = 2 * (size_t)kNumSM * (p->bm == kCpRows ? 1 : kCaWarps);
   p->ml_off = align_up(slots * p->bm * s.dh * 4);
   p->before_off = p->ml_off + align_up(slots * p->bm * 8);
   p->bytes = p->before_off + align_up(((size_t)c.B + 1) * 8);
@@ -2754,17 +2755,25 @@ whale_status plan_cache_attention(const Shape& s, const whale_cache& k, const wh
 }
 
 template <int DH, bool FP8, int MT>
-whale_status launch_attend_rows_t(const CacheAttnArgs& a, cudaStream_t st) {
+whale_status launch_attend_rows(const CacheAttnArgs& a, cudaStream_t st) {
   auto kern = cache_attend_kernel<DH, FP8, MT>;
   constexpr int smem = CaTile<DH, FP8>::SMEM;
   CUCHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   WCHECK(launch_pdl(kern, dim3(kNumSM), dim3(kCaThreads), smem, st, a));
-  return launch_pdl(cache_attend_merge_kernel<DH, 16 * MT>, dim3((unsigned)(a.c.B * a.c.kv_heads * a.n_qb)),
+  return launch_pdl(cache_attend_merge_kernel<DH, 16 * MT, false>, dim3((unsigned)(a.c.B * a.c.kv_heads * a.n_qb)),
                     dim3(kCaMergeThreads), 0, st, a, kNumSM * kCaWarps);
 }
 template <int DH, bool FP8>
-whale_status launch_attend_rows(const CacheAttnPlan& p, const CacheAttnArgs& a, cudaStream_t st) {
-  return p.bm == 16 ? launch_attend_rows_t<DH, FP8, 1>(a, st) : launch_attend_rows_t<DH, FP8, 2>(a, st);
+whale_status launch_attend(const CacheAttnPlan& p, const CacheAttnArgs& a, cudaStream_t st) {
+  if (p.bm == 16) return launch_attend_rows<DH, FP8, 1>(a, st);
+  if (p.bm == 32) return launch_attend_rows<DH, FP8, 2>(a, st);
+  auto kern = cache_attend_tc_kernel<DH, FP8>;
+  constexpr int smem = (int)CpSmem<DH>::BYTES;
+  CUCHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  WCHECK(launch_pdl(kern, dim3(kNumSM), dim3(kCpThreads), smem, st, a));
+  return launch_pdl(cache_attend_merge_kernel<DH, kCpRows, true>,
+                    dim3((unsigned)(a.c.B * a.c.kv_heads * a.n_qb), kCpRows / kCaMergeRows), dim3(kCaMergeThreads), 0, st,
+                    a, kNumSM);
 }
 
 whale_status cache_rows_call(const whale_config* cfg, const whale_cache* cache, const whale_chunk* chunk,
@@ -2948,8 +2957,8 @@ whale_status whale_cache_attention(const whale_config* cfg, const whale_cache* c
   p.before = reinterpret_cast<long long*>(static_cast<uint8_t*>(ws) + plan.before_off);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool fp8 = cache->format == WHALE_CACHE_E4M3;
-  if (s.dh == 32) return fp8 ? launch_attend_rows<32, true>(plan, p, st) : launch_attend_rows<32, false>(plan, p, st);
-  return fp8 ? launch_attend_rows<64, true>(plan, p, st) : launch_attend_rows<64, false>(plan, p, st);
+  if (s.dh == 32) return fp8 ? launch_attend<32, true>(plan, p, st) : launch_attend<32, false>(plan, p, st);
+  return fp8 ? launch_attend<64, true>(plan, p, st) : launch_attend<64, false>(plan, p, st);
 }
 
 whale_status whale_test_bounded_waits(unsigned long long limit_ns, whale_stream_t stream) {
