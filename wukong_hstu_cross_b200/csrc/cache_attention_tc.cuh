@@ -11,10 +11,10 @@
 // item, joined by cache_attend_merge_kernel in the order of the slices. Inside a CTA, for two tiles of 128 rows:
 //   warps 0-1   queries, and K and V of a unit, into 3 stages: bf16 by cp.async, e4m3 through registers, where
 //               number * 2^e becomes the bf16 number that it is. Rows in no page or past the end are zeros.
-//   warp 2      S = Q K^T (128 x 128, K = d_head) and O += P V (128 x d_head, K = 128) as their operands come
-//   warps 3-10  one thread per row: scores out of tensor memory, running maximum (the reference is raised when the
-//               tile's maximum exceeds it by 2^8, with the rescale of O in tensor memory then), weights to
-//               shared memory as bf16, sums in fp32; at an item's end O / l, or the partial.
+//   warps 2-3   a tile each: S = Q K^T (128 x 128, K = d_head) and O += P V (128 x d_head, K = 128)
+//   warps 4-11  one thread per row: scores out of tensor memory, running maximum (the reference is raised when the
+//               tile's maximum exceeds it by 2^8, with the rescale of O in tensor memory then), weights as bf16 back
+//               to tensor memory, where P V reads them, sums in fp32; at an item's end O / l, or the partial.
 #pragma once
 
 #include "cache_attention.cuh"
@@ -23,7 +23,12 @@ namespace whale {
 
 constexpr int kCpRows = 256;     // rows of an item: two tiles
 constexpr int kCpUnit = 128;     // positions of a unit
-constexpr int kCpThreads = 352;
+constexpr int kCpThreads = 384;       // three warpgroups, 168 registers a thread at launch
+// Registers afterwards: a row's 128 scores stay in a softmax thread's, a tile of raw e4m3 bytes in the producers'.
+constexpr int cp_regs_other(bool fp8) { return fp8 ? 120 : 88; }
+constexpr int cp_regs_softmax(bool fp8) { return fp8 ? 192 : 208; }
+static_assert(cp_regs_other(true) + 2 * cp_regs_softmax(true) <= 3 * 168 && cp_regs_other(false) + 2 * cp_regs_softmax(false) <= 3 * 168,
+              "the warpgroups share what the block was launched with");
 constexpr int kCpProducers = 64;
 constexpr int kCpMinUnits = 2;
 
@@ -31,12 +36,10 @@ template <int DH>
 struct CpSmem {
   static constexpr int ROW = 2 * DH;                         // bytes of a row of Q, K, V
   static constexpr uint32_t TILE = 128 * ROW;                // 128 rows
-  static constexpr int ST = 3;
-  static constexpr uint32_t P_TILE = 128 * 128 * 2;          // two blocks of 64 positions
+  static constexpr int ST = 4;
   static constexpr int OFF_Q = 0;                            // [2 buffers][2 tiles]
   static constexpr int OFF_KV = OFF_Q + 4 * (int)TILE;       // [ST][K, V]
-  static constexpr int OFF_P = OFF_KV + ST * 2 * (int)TILE;  // [2 tiles]
-  static constexpr int OFF_BAR = OFF_P + 2 * (int)P_TILE;
+  static constexpr int OFF_BAR = OFF_KV + ST * 2 * (int)TILE;
   // kvfull[ST], kvempty[ST], qfree[2], sfull[2], sfree[2], pfull[2], pfree[2], tmem slot, abort flag
   static constexpr size_t BYTES = 1024 + OFF_BAR + (2 * ST + 10) * 8 + 16;
   static_assert(BYTES <= 232448 - 1024, "shared memory of one CTA");
@@ -74,43 +77,70 @@ __device__ __forceinline__ long long cp_workers(long long T, long long W) {
   return w < W ? w : W;
 }
 
-// A CTA's slice, segment by segment; every role walks it for itself.
+// A CTA's slice, segment by segment; every warp walks it for itself (in shared memory: the softmax warps have no
+// registers to spare). Only the first segment is searched for: the next one begins the next item.
 struct CpWalk {
-  long long u, u_lo, u_hi, at, head_units;
-  int b;
-  CaSeq s;
-  // the segment
+  long long left;          // units after the present segment
+  int b, kvh, qb;
+  int t_lo, t_hi, units;   // the segment's units, and the item's
+  int n_rows, first;       // rows of the item; the slice's first segment
   long long pos0;
-  int kvh, qb, t_lo, t_hi, units, n_rows;
+  CaSeq s;
 
   __device__ __forceinline__ void sequence(const CacheAttnArgs& p, int b_) {
     b = b_;
     s = ca_seq(p, b, kCpRows);
-    head_units = cp_head_units(p, s, b, s.blocks);
     pos0 = (long long)p.c.lengths[b] - s.rows;
   }
-  __device__ __forceinline__ bool next(const CacheAttnArgs& p) {
-    if (u >= u_hi) return false;
-    while (u >= at + head_units * p.c.kv_heads) {
-      if (b + 1 >= p.c.B) return false;
-      at += head_units * p.c.kv_heads;
-      sequence(p, b + 1);
-    }
-    kvh = (int)((u - at) / head_units);
-    long long rem = (u - at) - kvh * head_units;
-    if (!p.causal) {
-      units = cp_units(p, s, pos0, 0);
-      qb = (int)(rem / units);
-      rem -= (long long)qb * units;
-    } else {
-      for (qb = 0; rem >= (units = cp_units(p, s, pos0, qb)); ++qb) rem -= units;
-    }
-    t_lo = (int)rem;
-    t_hi = (int)min((long long)units, t_lo + (u_hi - u));
+  __device__ __forceinline__ void item(const CacheAttnArgs& p, int from) {
+    units = cp_units(p, s, pos0, qb);
     n_rows = min(kCpRows, s.take * p.group - qb * kCpRows);
+    t_lo = from;
+    t_hi = (int)min((long long)units, t_lo + left);
+    left -= t_hi - t_lo;
+  }
+  // Unit u of the slice's sequence b_, whose units begin at `at`; n units to take.
+  __device__ __forceinline__ void begin(const CacheAttnArgs& p, int b_, long long at, long long u, long long n) {
+    sequence(p, b_);
+    const long long head = cp_head_units(p, s, b, s.blocks);
+    kvh = (int)((u - at) / head);
+    long long rem = u - at - kvh * head;
+    if (!p.causal) {
+      const int per = cp_units(p, s, pos0, 0);
+      qb = (int)(rem / per);
+      rem -= (long long)qb * per;
+    } else {
+      int per;
+      for (qb = 0; rem >= (per = cp_units(p, s, pos0, qb)); ++qb) rem -= per;
+    }
+    left = n;
+    first = 1;
+    item(p, (int)rem);
+  }
+  // One lane: to the next segment, if there is one.
+  __device__ __forceinline__ bool step(const CacheAttnArgs& p) {
+    if (left <= 0) return false;
+    first = 0;
+    if (++qb >= s.blocks) {
+      qb = 0;
+      if (++kvh >= p.c.kv_heads) {
+        kvh = 0;
+        do {
+          if (b + 1 >= p.c.B) return false;
+          sequence(p, b + 1);
+        } while (s.blocks == 0);
+      }
+    }
+    item(p, 0);
     return true;
   }
-  __device__ __forceinline__ void done() { u += t_hi - t_lo; }
+  // The whole warp. Begin with the present segment: do { .. } while (next(p)).
+  __device__ __forceinline__ bool next(const CacheAttnArgs& p) {
+    __syncwarp();
+    int more = 0;
+    if ((threadIdx.x & 31) == 0) more = step(p);
+    return __shfl_sync(0xffffffffu, more, 0);
+  }
 };
 
 // 2^x of two numbers on the FMA pipe, x <= 8: n = round(x) by the 1.5 * 2^23 trick, 2^(x - n) by the cubic of
@@ -149,6 +179,41 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// The MMAs of a whole warp, issued by one elected lane. _ts: A (M = 128 rows, 16 bf16 columns as 8 words a row)
+// in tensor memory.
+__device__ __forceinline__ void umma_f16_elect(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                               uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
+// The whole warp's wait: one answer, so that a wait that ran out ends every lane's work at the same place.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
+}
+
 template <int DH, bool FP8>
 __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __grid_constant__ CacheAttnArgs p) {
   using L = CpSmem<DH>;
@@ -170,10 +235,10 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
       mbar_init(&kvfull[s], kCpProducers / 32);
-      mbar_init(&kvempty[s], 1);
+      mbar_init(&kvempty[s], 2);  // both tiles
     }
     for (int h = 0; h < 2; ++h) {
-      mbar_init(&qfree[h], 1);
+      mbar_init(&qfree[h], 2);
       mbar_init(&sfull[h], 1);
       mbar_init(&sfree[h], 4);
       mbar_init(&pfull[h], 4);
@@ -218,15 +283,15 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
     T += sums[w];
   }
   const long long W = cp_workers(T, gridDim.x);
-  CpWalk walk;
-  walk.u_lo = walk.u = W > (long long)blockIdx.x ? (long long)blockIdx.x * T / W : T;
-  walk.u_hi = W > (long long)blockIdx.x ? ((long long)blockIdx.x + 1) * T / W : T;
+  __shared__ CpWalk walks[kCpThreads / 32];
+  const long long u_lo = W > (long long)blockIdx.x ? (long long)blockIdx.x * T / W : T;
+  const long long u_hi = W > (long long)blockIdx.x ? ((long long)blockIdx.x + 1) * T / W : T;
   {
     long long at = base + scan - mine;
     for (int b = b_lo; b < b_hi; ++b) {
       const long long n = seq_units(b);
       if (blockIdx.x == 0) p.before[b] = at;
-      if (at <= walk.u_lo && walk.u_lo < at + n) {
+      if (at <= u_lo && u_lo < at + n) {
         start_b = b;
         start_at = at;
       }
@@ -235,19 +300,23 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
     if (blockIdx.x == 0 && tid == kCpThreads - 1) p.before[p.c.B] = T;
   }
   __syncthreads();
-  if (walk.u < walk.u_hi) {
-    walk.at = start_at;
-    walk.sequence(p, start_b);
-  }
+  CpWalk& walk = walks[warp];
+  if (lane == 0 && u_lo < u_hi) walk.begin(p, start_b, start_at, u_lo, u_hi - u_lo);
+  __syncwarp();
 
-  if (warp < 2) {
+  if (u_lo >= u_hi) {
+    // no units: nothing but the common end
+  } else if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(cp_regs_other(FP8)));
+    if (warp < 2) {
     // ---------------- producers ----------------
     constexpr int CH = L::ROW / 16, RPI = 32 / CH;  // 16-byte chunks of a row, rows of a warp's instruction
     int n = 0, seg = 0;                             // tiles and segments so far
     bool ok = true;
     const long long v_off = p.c.planes == 2 ? (long long)p.c.kv_heads << p.c.page_shift : 0;
-    for (; ok && walk.next(p); walk.done(), ++seg) {
+    do {
       const long long kv_off = (long long)walk.kvh << p.c.page_shift;
+      const int t_lo = walk.t_lo, t_hi = walk.t_hi, len = walk.s.len, seq = walk.b;
       if (tid == 0 && p.c.lengths[walk.b] > walk.s.len) atomicOr(&g_device_error, kErrPages);
       if (tid == 0 && walk.s.rows > walk.s.take) atomicOr(&g_device_error, kErrOffsets);
       // rows (of each plane's first head) of this lane's two positions of unit i: the warp has 64 of the 128
@@ -257,16 +326,16 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
         for (int k = 0; k < 2; ++k) {
           const int pos = i * kCpUnit + warp * 64 + k * 32 + lane;
           at[k] = -1;
-          if (i < walk.t_hi && pos < walk.s.len) {
-            const long long r = cache_row(p.c, walk.b, pos);
+          if (i < t_hi && pos < len) {
+            const long long r = cache_row(p.c, seq, pos);
             if (r < 0) atomicOr(&g_device_error, kErrPages);
             else at[k] = r + kv_off;
           }
         }
       };
-      look(walk.t_lo);
+      look(t_lo);
       // queries into this segment's buffer
-      if (seg >= 2 && !mbar_wait(&qfree[seg & 1], ((seg >> 1) - 1) & 1, abort_flag)) break;
+      if (seg >= 2 && !warp_wait(&qfree[seg & 1], ((seg >> 1) - 1) & 1, abort_flag)) break;
       const uint32_t q_base = smem_u32(smem + L::OFF_Q) + (seg & 1) * 2 * L::TILE;
 #pragma unroll 4
       for (int k = 0; k < kCpRows / 2 / RPI; ++k) {
@@ -277,8 +346,8 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
                    p.q + (long long)(walk.s.first_row + tok) * p.ldq + head * DH + ch * 8, live ? 16u : 0u);
       }
       if constexpr (!FP8) {
-        for (int i = walk.t_lo; i < walk.t_hi; ++i, ++n) {
-          if (n >= ST && !mbar_wait(&kvempty[n % ST], (n / ST - 1) & 1, abort_flag)) {
+        for (int i = t_lo; i < t_hi; ++i, ++n) {
+          if (n >= ST && !warp_wait(&kvempty[n % ST], (n / ST - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -295,17 +364,12 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
             cp_async16(dst + L::TILE, a + (src < 0 ? 0 : v_off * L::ROW), bytes);
           }
           cp_async_commit();
-          if (i > walk.t_lo) {  // the tile before has arrived: hand it to the MMA
-            cp_async_wait<1>();
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&kvfull[(n - 1) % ST]);
-          }
+          // handed on at once: waiting to fill the next stage first would tie this tile to the P V two tiles back
+          cp_async_wait<0>();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&kvfull[n % ST]);
         }
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&kvfull[(n - 1) % ST]);
       } else {
         constexpr int RCH = DH / 16, RRPI = 32 / RCH, PASS = 64 / RRPI;  // raw rows are DH bytes
         uint4 raw[2][PASS];
@@ -328,9 +392,9 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
           }
         };
         load();
-        for (int i = walk.t_lo; i < walk.t_hi; ++i, ++n) {
+        for (int i = t_lo; i < t_hi; ++i, ++n) {
           look(i + 1);
-          if (n >= ST && !mbar_wait(&kvempty[n % ST], (n / ST - 1) & 1, abort_flag)) {
+          if (n >= ST && !warp_wait(&kvempty[n % ST], (n / ST - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -345,8 +409,8 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
               sts128(st + pl * L::TILE + L::at(r, 2 * ch + 1), cp_bf16x8(make_uint2(raw[pl][k].z, raw[pl][k].w), f));
             }
           }
-          if (i + 1 < walk.t_hi) load();
-          if (i == walk.t_lo) {  // the queries too
+          if (i + 1 < t_hi) load();
+          if (i == t_lo) {  // the queries too
             cp_async_commit();
             cp_async_wait<0>();
           }
@@ -355,103 +419,91 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
           if (lane == 0) mbar_arrive(&kvfull[n % ST]);
         }
       }
-    }
+      ++seg;
+    } while (ok && walk.next(p));
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == 2) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128);
-      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DH) | kIdescBMnMajor;
-      const uint32_t kv0 = smem_u32(smem + L::OFF_KV), q0 = smem_u32(smem + L::OFF_Q), p0 = smem_u32(smem + L::OFF_P);
-      int n = 0, seg = 0;         // tiles and segments so far
-      int c[2] = {0, 0};          // blocks of each tile so far (its barriers' phases)
-      bool ok = true;
-      for (; ok && walk.next(p); walk.done(), ++seg) {
-        const int blocks = walk.t_hi - walk.t_lo, tiles = walk.n_rows > 128 ? 2 : 1;
-        int si[2] = {0, tiles == 2 ? 0 : blocks}, pi[2] = {0, tiles == 2 ? 0 : blocks};  // next S, next P V of a tile
-        int freed = 0;
-        bool q_given = false;
-        uint64_t idle = 0;
-        while (freed < blocks) {
-          bool did = false;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (si[h] < blocks && si[h] <= pi[h] + 1) {
-              const int i = n + si[h];
-              if ((c[h] + si[h] == 0 || mbar_test(&sfree[h], (c[h] + si[h] - 1) & 1)) &&
-                  mbar_test(&kvfull[i % ST], (i / ST) & 1)) {
-                tc_fence_after();
-                const uint32_t k_base = kv0 + (i % ST) * 2 * L::TILE, q_base = q0 + ((seg & 1) * 2 + h) * L::TILE;
-#pragma unroll
-                for (int k = 0; k < DH / 16; ++k)
-                  umma_f16(tmem_base + h * 128, L::desc(q_base + k * 32), L::desc(k_base + k * 32), idesc_s, k > 0 ? 1u : 0u);
-                umma_commit(&sfull[h]);
-                ++si[h];
-                did = true;
-              }
-            }
-            if (pi[h] < si[h] && pi[h] < blocks && mbar_test(&pfull[h], (c[h] + pi[h]) & 1)) {
-              tc_fence_after();
-              const int i = n + pi[h];
-              const uint32_t v_base = kv0 + ((i % ST) * 2 + 1) * L::TILE, p_base = p0 + h * L::P_TILE;
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                umma_f16(tmem_base + 256 + h * 64, sdesc_k_sw128(p_base + (k >> 2) * 16384 + (k & 3) * 32),
-                         L::desc(v_base + k * 16 * L::ROW), idesc_pv, (pi[h] > 0 || k > 0) ? 1u : 0u);
-              umma_commit(&pfree[h]);
-              ++pi[h];
-              did = true;
-            }
-          }
-          if (!q_given && si[0] == blocks && si[1] == blocks) {
-            umma_commit(&qfree[seg & 1]);
-            q_given = true;
-          }
-          if (min(pi[0], pi[1]) > freed) {
-            umma_commit(&kvempty[(n + freed) % ST]);
-            ++freed;
-          }
-          if (did) {
-            idle = 0;
-          } else {
-            if (*abort_flag) {
-              ok = false;
-              break;
-            }
-            const uint64_t now = globaltimer_ns();
-            if (idle == 0) idle = now;
-            else if (now - idle > kWaitLimitNs) {
-              atomicOr(&g_device_error, kErrTimeout);
-              *abort_flag = 1;
-              ok = false;
-              break;
-            }
-          }
-        }
-        n += blocks;
-        c[0] += blocks;
-        if (tiles == 2) c[1] += blocks;
+    } else {
+    // ---------------- MMA issuers: warp 2 + h for tile h ----------------
+    // A unit's S as soon as the softmax warps have read the S before it, across segments too, then the P V of the
+    // unit before. The whole warp runs this with one lane elected per instruction, so that descriptors are uniform.
+    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DH) | kIdescBMnMajor;
+    const int h = warp - 2;
+    const uint32_t kv0 = smem_u32(smem + L::OFF_KV), q0 = smem_u32(smem + L::OFF_Q);
+    const uint32_t s_tm = tmem_base + h * 128, o_tm = tmem_base + 256 + h * 64, p_tm = tmem_base + 384 + h * 64;
+    int n = 0, seg = 0, c = 0;       // units, segments, and units that have this tile, so far
+    int late = -1;                   // unit whose P V is to come
+    bool late_first = false, ok = true;
+    auto flush = [&]() {
+      if (late < 0) return;
+      if (!warp_wait(&pfull[h], (c - 1) & 1, abort_flag)) {
+        ok = false;
+        return;
       }
+      tc_fence_after();
+      const uint32_t v_base = kv0 + ((late % ST) * 2 + 1) * L::TILE;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        umma_f16_ts(o_tm, p_tm + k * 8, L::desc(v_base + k * 16 * L::ROW), idesc_pv, !late_first || k > 0 ? 1u : 0u);
+      umma_commit_elect(&pfree[h]);
+      umma_commit_elect(&kvempty[late % ST]);
+      late = -1;
+    };
+    do {
+      const int blocks = walk.t_hi - walk.t_lo;
+      const bool active = walk.n_rows > 128 * h;
+      const uint32_t q_base = q0 + ((seg & 1) * 2 + h) * L::TILE;
+      for (int i = 0; i < blocks && ok; ++i, ++n) {
+        ok = warp_wait(&kvfull[n % ST], (n / ST) & 1, abort_flag);
+        if (!ok) break;
+        if (!active) {
+          flush();
+          if (lane == 0) {
+            mbar_arrive(&kvempty[n % ST]);
+            if (i == blocks - 1) mbar_arrive(&qfree[seg & 1]);
+          }
+          continue;
+        }
+        if (c > 0 && !warp_wait(&sfree[h], (c - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t k_base = kv0 + (n % ST) * 2 * L::TILE;
+#pragma unroll
+        for (int k = 0; k < DH / 16; ++k)
+          umma_f16_elect(s_tm, L::desc(q_base + k * 32), L::desc(k_base + k * 32), idesc_s, k > 0 ? 1u : 0u);
+        umma_commit_elect(&sfull[h]);
+        if (i == blocks - 1) umma_commit_elect(&qfree[seg & 1]);
+        flush();
+        late = n;
+        late_first = i == 0;
+        ++c;
+      }
+      ++seg;
+    } while (ok && walk.next(p));
+    if (ok) flush();
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(cp_regs_softmax(FP8)));
     // ---------------- softmax and output: one thread per row ----------------
-    const int q4 = warp & 3, h = (warp - 3) >> 2, row = q4 * 32 + lane;
+    const int q4 = warp & 3, h = (warp - 4) >> 2, row = q4 * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
     const uint32_t s_tm = tmem_base + h * 128 + lane_off, o_tm = tmem_base + 256 + h * 64 + lane_off;
-    const uint32_t p_row = smem_u32(smem + L::OFF_P) + h * L::P_TILE + row * 128;
+    const uint32_t p_tm = tmem_base + 384 + h * 64 + lane_off;  // weights, two a word
     int c = 0;  // blocks of this tile so far
     bool ok = true;
-    for (; ok && walk.next(p); walk.done()) {
+    do {
       if (walk.n_rows <= 128 * h) continue;
       const int blocks = walk.t_hi - walk.t_lo;
       const int r = 128 * h + row;
       const bool live = r < walk.n_rows;
-      const int srow = walk.qb * kCpRows + (live ? r : 0), tok = srow / p.group;
-      int end = walk.s.len;
-      if (p.causal) end = (int)max(0ll, min((long long)end, walk.pos0 + tok + 1));
+      int end = walk.s.len;  // of the positions from the segment's first on
+      if (p.causal) end = (int)max(0ll, min((long long)end, walk.pos0 + (walk.qb * kCpRows + (live ? r : 0)) / p.group + 1));
+      end -= walk.t_lo * kCpUnit;
       float m_run = -INFINITY, l = 0.f;
       for (int i = 0; i < blocks && ok; ++i, ++c) {
-        if (!mbar_wait(&sfull[h], c & 1, abort_flag)) {
+        if (!warp_wait(&sfull[h], c & 1, abort_flag)) {
           ok = false;
           break;
         }
@@ -465,7 +517,7 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sfree[h]);
-        const int nv = end - (walk.t_lo + i) * kCpUnit;  // positions of the block that this row sees
+        const int nv = end - i * kCpUnit;  // positions of the block that this row sees
         const bool full = __all_sync(0xffffffffu, nv >= kCpUnit);
         if (!full) {
 #pragma unroll
@@ -481,7 +533,7 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         const float m_new = mt > m_run + kCaLazy ? mt : m_run;
         // P of the block before has been read and O updated: P may be rewritten, O rescaled
-        if (i > 0 && !mbar_wait(&pfree[h], (c - 1) & 1, abort_flag)) {
+        if (i > 0 && !warp_wait(&pfree[h], (c - 1) & 1, abort_flag)) {
           ok = false;
           break;
         }
@@ -508,13 +560,14 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
           constexpr bool kFull = decltype(full_tag)::value;
           uint64_t ls[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
 #pragma unroll
-          for (int ch = 0; ch < 16; ++ch) {  // 16 chunks of 8 positions
-            uint32_t pk[4];
+          for (int half = 0; half < 2; ++half) {  // 64 positions each
+            uint32_t pk[32];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint64_t x = ffma2(f2pack(__uint_as_float(v[8 * ch + 2 * k]), __uint_as_float(v[8 * ch + 2 * k + 1])), sc2, nr2);
+            for (int k = 0; k < 32; ++k) {
+              const int j = 64 * half + 2 * k;
+              const uint64_t x = ffma2(f2pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sc2, nr2);
               float w0, w1;
-              if (kFull && (ch % 8 == 1 || ch % 8 == 4 || ch % 8 == 6)) {
+              if (kFull && k % 4 == 2) {  // between the others
                 cp_exp2(x, w0, w1);
               } else {
                 f2unpack(x, w0, w1);
@@ -524,7 +577,7 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
               ls[k & 1] = fadd2(ls[k & 1], f2pack(w0, w1));
               pk[k] = pack_bf16x2(w0, w1);
             }
-            sts128(p_row + (ch >> 3) * 16384 + (((ch & 7) ^ (row & 7)) << 4), make_uint4(pk[0], pk[1], pk[2], pk[3]));
+            tmem_st_32x32b_x32(p_tm + 32 * half, pk);
           }
           float a0, a1;
           f2unpack(fadd2(ls[0], ls[1]), a0, a1);
@@ -532,19 +585,20 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
         };
         if (full) exp_pass(std::true_type{});
         else exp_pass(std::false_type{});
-        fence_proxy_async_smem();
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pfull[h]);
       }
-      if (!ok || !mbar_wait(&pfree[h], (c - 1) & 1, abort_flag)) {
+      if (!ok || !warp_wait(&pfree[h], (c - 1) & 1, abort_flag)) {
         ok = false;
         break;
       }
       tc_fence_after();
       const bool whole = walk.t_lo == 0 && walk.t_hi == walk.units;
-      const long long slot = 2 * (long long)blockIdx.x + (walk.u != walk.u_lo);
+      const long long slot = 2 * (long long)blockIdx.x + !walk.first;
       const float f = whole ? (l == 0.f ? 0.f : 1.0f / l) : 1.f;
-      const int head = walk.kvh * p.group + srow % p.group;
+      const int srow = walk.qb * kCpRows + (live ? r : 0), tok = srow / p.group, head = walk.kvh * p.group + srow % p.group;
       __nv_bfloat16* dst = p.a + (long long)(walk.s.first_row + tok) * p.lda + head * DH;
       float* po = p.part_o + (slot * kCpRows + r) * DH;
 #pragma unroll 1
@@ -568,7 +622,7 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
       }
       if (live && !whole) *reinterpret_cast<float2*>(p.part_ml + (slot * kCpRows + r) * 2) = make_float2(m_run, l);
       tc_fence_before();
-    }
+    } while (ok && walk.next(p));
   }
 
   tc_fence_before();
