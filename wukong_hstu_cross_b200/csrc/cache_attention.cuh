@@ -45,8 +45,21 @@ struct CacheAttnArgs {
   float scale_log2;        // log2(e) / sqrt(d_head)
   float* part_o;           // [2 W, BM, DH]
   float* part_ml;          // [2 W, BM, 2]
-  long long* before;       // [B + 1] units before each sequence, and their number
+  struct CaCut* cuts;      // [W] the item that each slice leaves to the next ones
 };
+
+// An item that begins in a slice and does not end there: its rows, and the partials that make it up.
+struct CaCut {
+  int first_row, row0, n_rows, head0;  // packed row of the sequence, first row of the block, rows, first query head
+  int parts, slot;                     // slices (0: nothing to join), the first one's slot; the next ones' are 2 w
+  int pad[2];
+};
+__device__ __forceinline__ void ca_write_cut(CaCut* c, int first_row, int row0, int n_rows, int head0, int parts, int slot) {
+  reinterpret_cast<int4*>(c)[0] = make_int4(first_row, row0, n_rows, head0);
+  reinterpret_cast<int4*>(c)[1] = make_int4(parts, slot, 0, 0);
+}
+// Slice of W that holds unit u of T.
+__device__ __forceinline__ long long ca_slice_of(long long u, long long W, long long T) { return ((u + 1) * W - 1) / T; }
 
 constexpr int kCaTile = 32;     // positions of a unit
 constexpr int kCaWarps = 8;     // warps of a CTA (one CTA per SM)
@@ -159,21 +172,15 @@ __global__ void __launch_bounds__(kCaThreads, 1) cache_attend_kernel(const Cache
   __syncthreads();
   sums[tid + 1] = base + scan;
   if (tid == 0) sums[0] = 0;
-  if (blockIdx.x == 0) {  // for the merge
-    long long at = base + scan - mine;
-    for (int b = b_lo; b < b_hi; ++b) {
-      p.before[b] = at;
-      at += ca_units(p, b, BM);
-    }
-    if (tid == kCaThreads - 1) p.before[p.c.B] = base + scan;
-  }
   __syncthreads();
   const long long T = sums[kCaThreads];
   const long long W = ca_workers(T, (long long)gridDim.x * kCaWarps);
   const long long gw = (long long)warp * gridDim.x + blockIdx.x;  // neighbours on different SMs
-  if (gw >= W) return;
-  const long long u_lo = gw * T / W, u_hi = (gw + 1) * T / W;
-  if (u_lo >= u_hi) return;
+  const long long u_lo = gw < W ? gw * T / W : T, u_hi = gw < W ? (gw + 1) * T / W : T;
+  if (u_lo >= u_hi) {
+    if (lane == 0) ca_write_cut(p.cuts + gw, 0, 0, 0, 0, 0, 0);
+    return;
+  }
 
   // the sequence of the first unit
   int b, lo = 0, hi = kCaThreads - 1;
@@ -198,7 +205,10 @@ __global__ void __launch_bounds__(kCaThreads, 1) cache_attend_kernel(const Cache
     const CaSeq s = ca_seq(p, b, BM);
     const long long n_b = (long long)s.units * s.blocks * p.c.kv_heads;
     if (u >= at + n_b) {
-      if (b + 1 >= p.c.B) return;
+      if (b + 1 >= p.c.B) {  // cannot be: the units are the sequences'
+        if (lane == 0) ca_write_cut(p.cuts + gw, 0, 0, 0, 0, 0, 0);
+        return;
+      }
       at += n_b;
       ++b;
       continue;
@@ -566,6 +576,11 @@ __global__ void __launch_bounds__(kCaThreads, 1) cache_attend_kernel(const Cache
           *reinterpret_cast<float2*>(p.part_ml + (slot * BM + r) * 2) = make_float2(mr[m][hh], sum);
       }
     u += t_hi - t_lo;
+    if (u >= u_hi && lane == 0) {
+      const bool starts = !whole && t_lo == 0;
+      ca_write_cut(p.cuts + gw, s.first_row, r0, n_rows, kvh * p.group,
+                   starts ? (int)(ca_slice_of(u - t_hi + s.units - 1, W, T) - gw) + 1 : 0, (int)slot);
+    }
   }
 }
 

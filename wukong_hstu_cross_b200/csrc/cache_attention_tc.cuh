@@ -4,7 +4,7 @@
 //
 // Bound: the exponentials. A tile of 128 rows x 128 positions takes 16384 of them, 1024 cycles of the SM's
 // special-function units (16 a cycle), beside 2 * 128 * 128 * d_head multiply-adds in 128 (d_head 32) or 256 cycles
-// each. Three of every eight are therefore formed on the FMA pipe (cp_exp2), which leaves 640 cycles of either.
+// each. (A share of them on the FMA pipe gained nothing: a softmax warp is as busy with the rest of a score.)
 //
 // One CTA per SM takes a contiguous slice of the units (128 positions of one item = (sequence, K|V head, block of 256
 // rows)), all items' units laid end to end; causal items end at their last row's position. Partials where a slice cuts an
@@ -143,27 +143,6 @@ struct CpWalk {
   }
 };
 
-// 2^x of two numbers on the FMA pipe, x <= 8: n = round(x) by the 1.5 * 2^23 trick, 2^(x - n) by the cubic of
-// exp2_fma (relative error 7.5e-5, below the weights' rounding to bf16), n added to the exponent. Below -125: 2^-125.
-__device__ __forceinline__ void cp_exp2(uint64_t x, float& y0, float& y1) {
-  float x0, x1, t0, t1, p0, p1;
-  f2unpack(x, x0, x1);
-  asm("max.NaN.f32 %0, %0, 0fC2FA0000;" : "+f"(x0));  // -125; a NaN shows in the result
-  asm("max.NaN.f32 %0, %0, 0fC2FA0000;" : "+f"(x1));
-  const uint64_t xc = f2pack(x0, x1);
-  const uint64_t big = f2pack(12582912.0f, 12582912.0f);
-  const uint64_t t = fadd2(xc, big);
-  const uint64_t n = fadd2(t, f2pack(-12582912.0f, -12582912.0f));
-  const uint64_t f = ffma2(n, f2pack(-1.0f, -1.0f), xc);
-  uint64_t q = ffma2(f2pack(0.05517113208770752f, 0.05517113208770752f), f, f2pack(0.24261008203029633f, 0.24261008203029633f));
-  q = ffma2(q, f, f2pack(0.6932609677314758f, 0.6932609677314758f));
-  q = ffma2(q, f, f2pack(0.9999281167984009f, 0.9999281167984009f));
-  f2unpack(t, t0, t1);
-  f2unpack(q, p0, p1);
-  y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
-  y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
-}
-
 // Eight e4m3 numbers times 2^e as bf16 (exact).
 __device__ __forceinline__ uint4 cp_bf16x8(uint2 q, float f) {
   uint32_t o[4];
@@ -290,22 +269,20 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
     long long at = base + scan - mine;
     for (int b = b_lo; b < b_hi; ++b) {
       const long long n = seq_units(b);
-      if (blockIdx.x == 0) p.before[b] = at;
       if (at <= u_lo && u_lo < at + n) {
         start_b = b;
         start_at = at;
       }
       at += n;
     }
-    if (blockIdx.x == 0 && tid == kCpThreads - 1) p.before[p.c.B] = T;
   }
   __syncthreads();
   CpWalk& walk = walks[warp];
   if (lane == 0 && u_lo < u_hi) walk.begin(p, start_b, start_at, u_lo, u_hi - u_lo);
   __syncwarp();
 
-  if (u_lo >= u_hi) {
-    // no units: nothing but the common end
+  if (u_lo >= u_hi) {  // no units: nothing but the common end
+    if (tid == 0) ca_write_cut(p.cuts + blockIdx.x, 0, 0, 0, 0, 0, 0);
   } else if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(cp_regs_other(FP8)));
     if (warp < 2) {
@@ -494,8 +471,8 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
     int c = 0;  // blocks of this tile so far
     bool ok = true;
     do {
-      if (walk.n_rows <= 128 * h) continue;
       const int blocks = walk.t_hi - walk.t_lo;
+      if (walk.n_rows <= 128 * h) continue;
       const int r = 128 * h + row;
       const bool live = r < walk.n_rows;
       int end = walk.s.len;  // of the positions from the segment's first on
@@ -532,12 +509,13 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
             mx[k] = fmax3(mx[k], __uint_as_float(v[j + 2 * k]), __uint_as_float(v[j + 2 * k + 1]));
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         const float m_new = mt > m_run + kCaLazy ? mt : m_run;
-        // P of the block before has been read and O updated: P may be rewritten, O rescaled
-        if (i > 0 && !warp_wait(&pfree[h], (c - 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
+        bool may_write = i == 0;  // P of the block before has been read and O updated
         if (i > 0 && __any_sync(0xffffffffu, m_new != m_run)) {
+          if (!warp_wait(&pfree[h], (c - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          may_write = true;
           tc_fence_after();
           const float f = m_new == m_run ? 1.f : fast_exp2(m_run - m_new);
 #pragma unroll 1
@@ -556,8 +534,7 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
         m_run = m_new;
         const float ref = m_run == -INFINITY ? 0.f : m_run;
         const uint64_t sc2 = f2pack(p.scale_log2, p.scale_log2), nr2 = f2pack(-ref, -ref);
-        auto exp_pass = [&](auto full_tag) {
-          constexpr bool kFull = decltype(full_tag)::value;
+        {
           uint64_t ls[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
 #pragma unroll
           for (int half = 0; half < 2; ++half) {  // 64 positions each
@@ -567,24 +544,22 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
               const int j = 64 * half + 2 * k;
               const uint64_t x = ffma2(f2pack(__uint_as_float(v[j]), __uint_as_float(v[j + 1])), sc2, nr2);
               float w0, w1;
-              if (kFull && k % 4 == 2) {  // between the others
-                cp_exp2(x, w0, w1);
-              } else {
-                f2unpack(x, w0, w1);
-                w0 = fast_exp2(w0);
-                w1 = fast_exp2(w1);
-              }
+              f2unpack(x, w0, w1);
+              w0 = fast_exp2(w0);
+              w1 = fast_exp2(w1);
               ls[k & 1] = fadd2(ls[k & 1], f2pack(w0, w1));
               pk[k] = pack_bf16x2(w0, w1);
+            }
+            if (half == 0 && !may_write) {
+              if (!warp_wait(&pfree[h], (c - 1) & 1, abort_flag)) ok = false;
+              tc_fence_after();
             }
             tmem_st_32x32b_x32(p_tm + 32 * half, pk);
           }
           float a0, a1;
           f2unpack(fadd2(ls[0], ls[1]), a0, a1);
           l += a0 + a1;
-        };
-        if (full) exp_pass(std::true_type{});
-        else exp_pass(std::false_type{});
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -621,6 +596,11 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
         }
       }
       if (live && !whole) *reinterpret_cast<float2*>(p.part_ml + (slot * kCpRows + r) * 2) = make_float2(m_run, l);
+      if (r == 0 && walk.left <= 0) {  // the slice's last segment
+        const long long u0 = u_hi - walk.t_hi;  // the item's first unit
+        ca_write_cut(p.cuts + blockIdx.x, walk.s.first_row, walk.qb * kCpRows, walk.n_rows, walk.kvh * p.group,
+                     !whole && walk.t_lo == 0 ? (int)(ca_slice_of(u0 + walk.units - 1, W, T) - blockIdx.x) + 1 : 0, (int)slot);
+      }
       tc_fence_before();
     } while (ok && walk.next(p));
   }
@@ -633,59 +613,44 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
   }
 }
 
-// One CTA per (sequence, K|V head, row block) and kCaMergeRows of its rows: joins the partials of the item, if it was
-// cut, in the order of the slices. TC: those of cache_attend_tc_kernel (blocks of 256 rows), else cache_attend_kernel's.
+// One CTA per slice and kCaMergeRows rows: joins the partials of the item that begins in the slice and does not end
+// there, in the order of the slices.
 constexpr int kCaMergeThreads = 256, kCaMergeRows = 32;
-template <int DH, int BM, bool TC>
-__global__ void __launch_bounds__(kCaMergeThreads) cache_attend_merge_kernel(const CacheAttnArgs p, int workers) {
+template <int DH, int BM>
+__global__ void __launch_bounds__(kCaMergeThreads) cache_attend_merge_kernel(const CacheAttnArgs p) {
   __shared__ float4 so[kCaMergeThreads];
   __shared__ float2 sml[kCaMergeThreads];
   pdl_wait();
   pdl_trigger();
-  const int qb = blockIdx.x % p.n_qb, kvh = blockIdx.x / p.n_qb % p.c.kv_heads, b = blockIdx.x / (p.n_qb * p.c.kv_heads);
-  const CaSeq s = ca_seq(p, b, BM);
-  if (qb >= s.blocks) return;
-  const int row0 = blockIdx.y * kCaMergeRows;  // first row in the block
-  const int n_rows = min(kCaMergeRows, min(BM, s.take * p.group - qb * BM) - row0);
-  if (n_rows <= 0) return;
-  const long long T = p.before[p.c.B], W = TC ? cp_workers(T, workers) : ca_workers(T, workers);
-  long long u0 = p.before[b], units = s.units;
-  if constexpr (TC) {
-    const long long pos0 = (long long)p.c.lengths[b] - s.rows;
-    units = cp_units(p, s, pos0, qb);
-    u0 += kvh * cp_head_units(p, s, b, s.blocks) + cp_head_units(p, s, b, qb);
-  } else {
-    u0 += (long long)(kvh * s.blocks + qb) * units;
-  }
-  const long long u1 = u0 + units - 1;
-  const long long w0 = ((u0 + 1) * W - 1) / T, w1 = ((u1 + 1) * W - 1) / T;
-  if (w0 == w1) return;
-  const int n = (int)(w1 - w0 + 1);
+  const int4 c0 = reinterpret_cast<const int4*>(p.cuts + blockIdx.x)[0], c1 = reinterpret_cast<const int4*>(p.cuts + blockIdx.x)[1];
+  const int first_row = c0.x, head0 = c0.w, n = c1.x, slot0 = c1.y;
+  const int row0 = blockIdx.y * kCaMergeRows, n_rows = min(kCaMergeRows, c0.z - row0);  // of the block
+  if (n <= 1 || n_rows <= 0) return;
   const int vecs = n_rows * (DH / 4);
   // `groups` threads take every groups-th partial of one vector of 4 columns
   int groups = 1;
   while (groups * 2 * vecs <= kCaMergeThreads && groups < n) groups *= 2;
   const int per = kCaMergeThreads / groups, grp = threadIdx.x / per;
+  auto join = [](float& m, float& l, float4& o, const float2& ml, const float4& x) {
+    const float mn = fmaxf(m, ml.x);
+    const float fo = m == mn ? 1.f : fast_exp2(m - mn), fx = ml.x == mn ? 1.f : fast_exp2(ml.x - mn);
+    m = mn;
+    l = l * fo + ml.y * fx;
+    o.x = o.x * fo + x.x * fx;
+    o.y = o.y * fo + x.y * fx;
+    o.z = o.z * fo + x.z * fx;
+    o.w = o.w * fo + x.w * fx;
+  };
   for (int v0 = 0; v0 < vecs; v0 += per) {
-    const int v = v0 + threadIdx.x % per;
+    const int v = v0 + threadIdx.x % per, r = v / (DH / 4), c4 = v % (DH / 4);
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int r = v / (DH / 4), c4 = v % (DH / 4);
     if (v < vecs) {
 #pragma unroll 4
       for (int k = grp; k < n; k += groups) {
-        const long long w = w0 + k;
-        const long long slot = (2 * w + (w * T / W < u0 ? 1 : 0)) * BM + row0 + r;
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot * 2);
-        const float4 x = *reinterpret_cast<const float4*>(p.part_o + slot * DH + 4 * c4);
-        const float mn = fmaxf(m, ml.x);
-        const float fo = m == mn ? 1.f : fast_exp2(m - mn), fx = ml.x == mn ? 1.f : fast_exp2(ml.x - mn);
-        m = mn;
-        l = l * fo + ml.y * fx;
-        o.x = o.x * fo + x.x * fx;
-        o.y = o.y * fo + x.y * fx;
-        o.z = o.z * fo + x.z * fx;
-        o.w = o.w * fo + x.w * fx;
+        const long long slot = (long long)(k == 0 ? slot0 : 2 * ((int)blockIdx.x + k)) * BM + row0 + r;
+        join(m, l, o, *reinterpret_cast<const float2*>(p.part_ml + slot * 2),
+             *reinterpret_cast<const float4*>(p.part_o + slot * DH + 4 * c4));
       }
     }
     if (groups > 1) {  // one round: vecs <= per
@@ -693,23 +658,12 @@ __global__ void __launch_bounds__(kCaMergeThreads) cache_attend_merge_kernel(con
       sml[threadIdx.x] = make_float2(m, l);
       __syncthreads();
       if (grp == 0 && v < vecs)
-        for (int k = 1; k < groups; ++k) {
-          const float2 ml = sml[k * per + v];
-          const float4 x = so[k * per + v];
-          const float mn = fmaxf(m, ml.x);
-          const float fo = m == mn ? 1.f : fast_exp2(m - mn), fx = ml.x == mn ? 1.f : fast_exp2(ml.x - mn);
-          m = mn;
-          l = l * fo + ml.y * fx;
-          o.x = o.x * fo + x.x * fx;
-          o.y = o.y * fo + x.y * fx;
-          o.z = o.z * fo + x.z * fx;
-          o.w = o.w * fo + x.w * fx;
-        }
+        for (int k = 1; k < groups; ++k) join(m, l, o, sml[k * per + v], so[k * per + v]);
     }
     if (grp == 0 && v < vecs) {
       const float f = l == 0.f ? 0.f : 1.f / l;
-      const int row = qb * BM + row0 + r, tok = row / p.group, head = kvh * p.group + row % p.group;
-      *reinterpret_cast<uint2*>(p.a + (long long)(s.first_row + tok) * p.lda + head * DH + 4 * c4) =
+      const int row = c0.y + row0 + r, tok = row / p.group, head = head0 + row % p.group;
+      *reinterpret_cast<uint2*>(p.a + (long long)(first_row + tok) * p.lda + head * DH + 4 * c4) =
           make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
     }
   }

@@ -2736,7 +2736,7 @@ whale_status launch_rows(bool append, RowsArgs a, cudaStream_t st) {
 // Row blocks and workspace of the attention over the cache.
 struct CacheAttnPlan {
   int bm, n_qb, max_new;
-  size_t ml_off, before_off, bytes;
+  size_t ml_off, cuts_off, bytes;
 };
 whale_status plan_cache_attention(const Shape& s, const whale_cache& k, const whale_chunk& c, CacheAttnPlan* p) {
   const int group = s.h / k.n_kv_heads;
@@ -2746,11 +2746,10 @@ whale_status plan_cache_attention(const Shape& s, const whale_cache& k, const wh
   // rows and positions are counted in 32 bits in the kernels
   if (c.total_new * s.h >= (1ll << 31) || c.max_length > (1 << 30)) return WHALE_ERR_UNSUPPORTED;
   p->n_qb = (int)std::max(1ll, cdiv<long long>(rows, p->bm));
-  if ((double)c.B * k.n_kv_heads * p->n_qb >= 2147483647.0) return WHALE_ERR_UNSUPPORTED;
-  const size_t slots = 2 * (size_t)kNumSM * (p->bm == kCpRows ? 1 : kCaWarps);
+  const size_t slices = (size_t)kNumSM * (p->bm == kCpRows ? 1 : kCaWarps), slots = 2 * slices;
   p->ml_off = align_up(slots * p->bm * s.dh * 4);
-  p->before_off = p->ml_off + align_up(slots * p->bm * 8);
-  p->bytes = p->before_off + align_up(((size_t)c.B + 1) * 8);
+  p->cuts_off = p->ml_off + align_up(slots * p->bm * 8);
+  p->bytes = p->cuts_off + align_up(slices * sizeof(CaCut));
   return WHALE_OK;
 }
 
@@ -2760,8 +2759,7 @@ whale_status launch_attend_rows(const CacheAttnArgs& a, cudaStream_t st) {
   constexpr int smem = CaTile<DH, FP8>::SMEM;
   CUCHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   WCHECK(launch_pdl(kern, dim3(kNumSM), dim3(kCaThreads), smem, st, a));
-  return launch_pdl(cache_attend_merge_kernel<DH, 16 * MT, false>, dim3((unsigned)(a.c.B * a.c.kv_heads * a.n_qb)),
-                    dim3(kCaMergeThreads), 0, st, a, kNumSM * kCaWarps);
+  return launch_pdl(cache_attend_merge_kernel<DH, 16 * MT>, dim3(kNumSM * kCaWarps), dim3(kCaMergeThreads), 0, st, a);
 }
 template <int DH, bool FP8>
 whale_status launch_attend(const CacheAttnPlan& p, const CacheAttnArgs& a, cudaStream_t st) {
@@ -2771,9 +2769,7 @@ whale_status launch_attend(const CacheAttnPlan& p, const CacheAttnArgs& a, cudaS
   constexpr int smem = (int)CpSmem<DH>::BYTES;
   CUCHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   WCHECK(launch_pdl(kern, dim3(kNumSM), dim3(kCpThreads), smem, st, a));
-  return launch_pdl(cache_attend_merge_kernel<DH, kCpRows, true>,
-                    dim3((unsigned)(a.c.B * a.c.kv_heads * a.n_qb), kCpRows / kCaMergeRows), dim3(kCaMergeThreads), 0, st,
-                    a, kNumSM);
+  return launch_pdl(cache_attend_merge_kernel<DH, kCpRows>, dim3(kNumSM, kCpRows / kCaMergeRows), dim3(kCaMergeThreads), 0, st, a);
 }
 
 whale_status cache_rows_call(const whale_config* cfg, const whale_cache* cache, const whale_chunk* chunk,
@@ -2954,7 +2950,7 @@ whale_status whale_cache_attention(const whale_config* cfg, const whale_cache* c
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s.dh));
   p.part_o = static_cast<float*>(ws);
   p.part_ml = p.part_o + plan.ml_off / 4;
-  p.before = reinterpret_cast<long long*>(static_cast<uint8_t*>(ws) + plan.before_off);
+  p.cuts = reinterpret_cast<CaCut*>(static_cast<uint8_t*>(ws) + plan.cuts_off);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const bool fp8 = cache->format == WHALE_CACHE_E4M3;
   if (s.dh == 32) return fp8 ? launch_attend<32, true>(plan, p, st) : launch_attend<32, false>(plan, p, st);
