@@ -56,22 +56,20 @@ struct CpSmem {
   }
 };
 
-// Units of one (K|V head, block of ROWS rows) of a sequence, and of all its row blocks.
-template <int ROWS>
+// Units of one (K|V head, row block) of a sequence, and of all its row blocks.
 __device__ __forceinline__ int cp_units(const CacheAttnArgs& p, const CaSeq& s, long long pos0, int qb) {
   long long e = s.len;
   if (p.causal) {
-    const int last = (min(s.take * p.group, (qb + 1) * ROWS) - 1) / p.group;
+    const int last = (min(s.take * p.group, (qb + 1) * kCpRows) - 1) / p.group;
     e = min(e, pos0 + last + 1);
   }
   return e <= kCpUnit ? 1 : (int)((e + kCpUnit - 1) / kCpUnit);
 }
-template <int ROWS>
 __device__ __forceinline__ long long cp_head_units(const CacheAttnArgs& p, const CaSeq& s, int b, int blocks) {
-  if (!p.causal) return blocks ? (long long)blocks * cp_units<ROWS>(p, s, 0, 0) : 0;
+  if (!p.causal) return blocks ? (long long)blocks * cp_units(p, s, 0, 0) : 0;
   const long long pos0 = (long long)p.c.lengths[b] - s.rows;
   long long n = 0;
-  for (int qb = 0; qb < blocks; ++qb) n += cp_units<ROWS>(p, s, pos0, qb);
+  for (int qb = 0; qb < blocks; ++qb) n += cp_units(p, s, pos0, qb);
   return n;
 }
 __device__ __forceinline__ long long cp_workers(long long T, long long W) {
@@ -81,7 +79,6 @@ __device__ __forceinline__ long long cp_workers(long long T, long long W) {
 
 // A CTA's slice, segment by segment; every warp walks it for itself (in shared memory: the softmax warps have no
 // registers to spare). Only the first segment is searched for: the next one begins the next item.
-template <int ROWS>
 struct CpWalk {
   long long left;          // units after the present segment
   int b, kvh, qb;
@@ -92,12 +89,12 @@ struct CpWalk {
 
   __device__ __forceinline__ void sequence(const CacheAttnArgs& p, int b_) {
     b = b_;
-    s = ca_seq(p, b, ROWS);
+    s = ca_seq(p, b, kCpRows);
     pos0 = (long long)p.c.lengths[b] - s.rows;
   }
   __device__ __forceinline__ void item(const CacheAttnArgs& p, int from) {
-    units = cp_units<ROWS>(p, s, pos0, qb);
-    n_rows = min(ROWS, s.take * p.group - qb * ROWS);
+    units = cp_units(p, s, pos0, qb);
+    n_rows = min(kCpRows, s.take * p.group - qb * kCpRows);
     t_lo = from;
     t_hi = (int)min((long long)units, t_lo + left);
     left -= t_hi - t_lo;
@@ -105,16 +102,16 @@ struct CpWalk {
   // Unit u of the slice's sequence b_, whose units begin at `at`; n units to take.
   __device__ __forceinline__ void begin(const CacheAttnArgs& p, int b_, long long at, long long u, long long n) {
     sequence(p, b_);
-    const long long head = cp_head_units<ROWS>(p, s, b, s.blocks);
+    const long long head = cp_head_units(p, s, b, s.blocks);
     kvh = (int)((u - at) / head);
     long long rem = u - at - kvh * head;
     if (!p.causal) {
-      const int per = cp_units<ROWS>(p, s, pos0, 0);
+      const int per = cp_units(p, s, pos0, 0);
       qb = (int)(rem / per);
       rem -= (long long)qb * per;
     } else {
       int per;
-      for (qb = 0; rem >= (per = cp_units<ROWS>(p, s, pos0, qb)); ++qb) rem -= per;
+      for (qb = 0; rem >= (per = cp_units(p, s, pos0, qb)); ++qb) rem -= per;
     }
     left = n;
     first = 1;
@@ -145,58 +142,6 @@ struct CpWalk {
     return __shfl_sync(0xffffffffu, more, 0);
   }
 };
-
-// The block's slice [u_lo, u_hi) of T units over W workers, and the sequence that holds u_lo (its first unit: at).
-template <int THREADS>
-struct CpSlice {
-  long long sums[THREADS / 32];
-  long long T, W, u_lo, u_hi, at;
-  int b;
-};
-// Units before each thread's run of sequences by a scan over the block; ends with a barrier.
-template <int ROWS, int THREADS>
-__device__ __forceinline__ void cp_slice(const CacheAttnArgs& p, CpSlice<THREADS>& o) {
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int run = (p.c.B + THREADS - 1) / THREADS;
-  const int b_lo = min(p.c.B, tid * run), b_hi = min(p.c.B, b_lo + run);
-  auto seq_units = [&](int b) {
-    const CaSeq s = ca_seq(p, b, ROWS);
-    return cp_head_units<ROWS>(p, s, b, s.blocks) * p.c.kv_heads;
-  };
-  long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += seq_units(b);
-  long long scan = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, scan, d);
-    if (lane >= d) scan += v;
-  }
-  if (lane == 31) o.sums[warp] = scan;
-  __syncthreads();
-  long long base = 0, T = 0;
-  for (int w = 0; w < THREADS / 32; ++w) {
-    base += w < warp ? o.sums[w] : 0;
-    T += o.sums[w];
-  }
-  const long long W = cp_workers(T, gridDim.x), w = blockIdx.x;
-  const long long u_lo = w < W ? w * T / W : T, u_hi = w < W ? (w + 1) * T / W : T;
-  if (tid == 0) {
-    o.T = T;
-    o.W = W;
-    o.u_lo = u_lo;
-    o.u_hi = u_hi;
-  }
-  long long at = base + scan - mine;
-  for (int b = b_lo; b < b_hi; ++b) {
-    const long long n = seq_units(b);
-    if (at <= u_lo && u_lo < at + n) {
-      o.b = b;
-      o.at = at;
-    }
-    at += n;
-  }
-  __syncthreads();
-}
 
 // Eight e4m3 numbers times 2^e as bf16 (exact).
 __device__ __forceinline__ uint4 cp_bf16x8(uint2 q, float f) {
@@ -253,6 +198,7 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
   using L = CpSmem<DH>;
   constexpr int ST = L::ST;
   extern __shared__ uint8_t smem_raw[];
+  __shared__ long long sums[kCpThreads / 32 + 1];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* kvfull = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
   uint64_t* kvempty = kvfull + ST;
@@ -288,15 +234,51 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
   pdl_wait();
   pdl_trigger();
 
-  __shared__ CpSlice<kCpThreads> slice;
-  __shared__ CpWalk<kCpRows> walks[kCpThreads / 32];
+  // units before each thread's run of sequences; the slice; its first sequence
+  __shared__ int start_b;
+  __shared__ long long start_at;
+  const int run = (p.c.B + kCpThreads - 1) / kCpThreads;
+  const int b_lo = min(p.c.B, tid * run), b_hi = min(p.c.B, b_lo + run);
+  auto seq_units = [&](int b) {
+    const CaSeq s = ca_seq(p, b, kCpRows);
+    return cp_head_units(p, s, b, s.blocks) * p.c.kv_heads;
+  };
+  long long mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += seq_units(b);
+  long long scan = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) sums[warp] = scan;
   tc_fence_before();
-  cp_slice<kCpRows, kCpThreads>(p, slice);
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const long long T = slice.T, W = slice.W, u_lo = slice.u_lo, u_hi = slice.u_hi;
-  CpWalk<kCpRows>& walk = walks[warp];
-  if (lane == 0 && u_lo < u_hi) walk.begin(p, slice.b, slice.at, u_lo, u_hi - u_lo);
+  long long base = 0, T = 0;
+  for (int w = 0; w < kCpThreads / 32; ++w) {
+    base += w < warp ? sums[w] : 0;
+    T += sums[w];
+  }
+  const long long W = cp_workers(T, gridDim.x);
+  __shared__ CpWalk walks[kCpThreads / 32];
+  const long long u_lo = W > (long long)blockIdx.x ? (long long)blockIdx.x * T / W : T;
+  const long long u_hi = W > (long long)blockIdx.x ? ((long long)blockIdx.x + 1) * T / W : T;
+  {
+    long long at = base + scan - mine;
+    for (int b = b_lo; b < b_hi; ++b) {
+      const long long n = seq_units(b);
+      if (at <= u_lo && u_lo < at + n) {
+        start_b = b;
+        start_at = at;
+      }
+      at += n;
+    }
+  }
+  __syncthreads();
+  CpWalk& walk = walks[warp];
+  if (lane == 0 && u_lo < u_hi) walk.begin(p, start_b, start_at, u_lo, u_hi - u_lo);
   __syncwarp();
 
   if (u_lo >= u_hi) {  // no units: nothing but the common end

@@ -36,7 +36,6 @@
 #include "attention_bwd_tc.cuh"
 #include "backward.cuh"
 #include "cache_attention.cuh"
-#include "cache_attention_e4m3.cuh"
 #include "cache_attention_tc.cuh"
 #include "fp32_path.cuh"
 #include "gemm_2sm.cuh"
@@ -2765,15 +2764,7 @@ whale_status launch_attend_rows(const CacheAttnArgs& a, cudaStream_t st) {
 template <int DH, bool FP8>
 whale_status launch_attend(const CacheAttnPlan& p, const CacheAttnArgs& a, cudaStream_t st) {
   if (p.bm == 16) return launch_attend_rows<DH, FP8, 1>(a, st);
-  if (p.bm == 32 && !FP8) return launch_attend_rows<DH, FP8, 2>(a, st);
-  if constexpr (FP8) {
-    if (p.bm == 32) {
-      constexpr int blocks = kCeBlocksPerSM * kNumSM, bytes = (int)CeSmem<DH>::BYTES;
-      CUCHECK(cudaFuncSetAttribute(cache_attend_e4m3_kernel<DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-      WCHECK(launch_pdl(cache_attend_e4m3_kernel<DH>, dim3(blocks), dim3(kCeThreads), bytes, st, a));
-      return launch_pdl(cache_attend_merge_kernel<DH, kCeRows>, dim3(blocks), dim3(kCaMergeThreads), 0, st, a);
-    }
-  }
+  if (p.bm == 32) return launch_attend_rows<DH, FP8, 2>(a, st);
   auto kern = cache_attend_tc_kernel<DH, FP8>;
   constexpr int smem = (int)CpSmem<DH>::BYTES;
   CUCHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
