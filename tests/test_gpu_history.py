@@ -467,6 +467,9 @@ ATTEND = [  # lengths, new, h, hk, dh, page, shared
     ([400, 513], [200, 300], 8, 2, 32, 32, False),
     ([700, 300, 0, 9], [300, 129, 0, 9], 4, 1, 64, 128, True),
     ([600, 256], [255, 128], 4, 4, 32, 256, False),
+    ([640, 0, 3, 129, 5000], [17, 4, 20, 0, 32], 8, 8, 32, 16, False),
+    ([2000, 128, 127], [8, 7, 1], 8, 2, 64, 32, True),
+    ([1537] * 4, [29, 1, 32, 2], 2, 2, 32, 512, True),
 ]
 
 

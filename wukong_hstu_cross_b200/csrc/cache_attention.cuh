@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) cache_attend_kernel(const Cache
   constexpr int BM = 16 * MT, NT = kCaTile / 8, KS = DH / 16, ND = DH / 8, STAGES = L::STAGES;
   extern __shared__ __align__(128) uint8_t ring_all[];
   __shared__ long long sums[kCaThreads + 1];
+  __shared__ __align__(16) float factors[kCaWarps][2 * kCaTile];  // e4m3: K's and V's factor of each position of a unit
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   pdl_wait();
@@ -291,7 +292,8 @@ __global__ void __launch_bounds__(kCaThreads, 1) cache_attend_kernel(const Cache
     const long long kv_off = (long long)kvh << p.c.page_shift;
     const uint32_t vpl = p.c.planes == 2 ? L::PLANE : 0;  // V's plane of a stage (K's with shared K = V)
     const long long v_off = p.c.planes == 2 ? (long long)p.c.kv_heads << p.c.page_shift : 0;
-    auto look = [&](int i) -> long long {
+    const long long v_bytes = v_off * L::ROW;
+    auto look = [&](int i) -> int {  // rows of the pool are numbered in 31 bits
       const int pos = i * kCaTile + lane;
       if (i >= t_hi || pos >= s.len) return -1;
       const long long r = cache_row(p.c, b, pos);
@@ -299,23 +301,23 @@ __global__ void __launch_bounds__(kCaThreads, 1) cache_attend_kernel(const Cache
         atomicOr(&g_device_error, kErrPages);
         return -1;
       }
-      return r + kv_off;
+      return (int)(r + kv_off);
     };
-    auto fetch = [&](int i, long long row) {  // tile i, whose lane's row is `row`
+    auto fetch = [&](int i, int row) {  // tile i, whose lane's row is `row`
       if (i >= t_hi) return;
       const uint32_t st = ring + (uint32_t)((i - t_lo) % STAGES) * L::BYTES;
       constexpr int CH = L::ROW / 16, RPI = 32 / CH;  // 16-byte chunks of a row, rows of one instruction
 #pragma unroll
       for (int k = 0; k < kCaTile / RPI; ++k) {
         const int r = k * RPI + lane / CH, ch = lane % CH;
-        const long long src = __shfl_sync(0xffffffffu, row, r);
+        const int src = __shfl_sync(0xffffffffu, row, r);
         const uint32_t n = src < 0 ? 0u : 16u;
-        const uint8_t* a = pages + (src < 0 ? 0 : src) * L::ROW + ch * 16;
+        const uint8_t* a = pages + (long long)max(src, 0) * L::ROW + ch * 16;
         cp_async16(st + L::at(r, ch), a, n);
-        if (vpl) cp_async16(st + L::PLANE + L::at(r, ch), a + (src < 0 ? 0 : v_off * L::ROW), n);
+        if (vpl) cp_async16(st + L::PLANE + L::at(r, ch), src < 0 ? a : a + v_bytes, n);
       }
       if constexpr (FP8) {
-        const long long src = __shfl_sync(0xffffffffu, row, 4 * (lane & 7));
+        const int src = __shfl_sync(0xffffffffu, row, 4 * (lane & 7));
         if (lane < 16 && src < 0)  // rows in no page are zeros: any scale will do, but not a stale one
           asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + 2 * L::PLANE + (lane >> 3) * kCaTile + 4 * (lane & 7)), "r"(0u)
                        : "memory");
@@ -330,7 +332,7 @@ __global__ void __launch_bounds__(kCaThreads, 1) cache_attend_kernel(const Cache
       fetch(t_lo + i, look(t_lo + i));
       cp_async_commit();
     }
-    long long ahead = look(t_lo + STAGES - 1);
+    int ahead = look(t_lo + STAGES - 1);
 
     for (int i = t_lo; i < t_hi; ++i) {
       cp_async_wait<STAGES - 2>();
@@ -386,13 +388,14 @@ __global__ void __launch_bounds__(kCaThreads, 1) cache_attend_kernel(const Cache
       }
 
       // scales: K's into the scores, V's as factors of the weights (8 neighbouring positions a lane)
-      float vf[2 * NT];
+      uint64_t vf[NT];  // pairs
       if constexpr (FP8) {
-        const uint2 kc = lds64(st + 2 * L::PLANE + 8 * t), vc = lds64(st + 2 * L::PLANE + kCaTile + 8 * t);
         const bool ok = pos + lane < s.len;  // rows past the end hold any code
-        uint32_t code;
-        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(st + 2 * L::PLANE + kCaTile + lane));
-        const int e_new = max(e_ref, (int)__reduce_max_sync(0xffffffffu, ok ? code : 0u));
+        uint32_t ck, cv;
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(ck) : "r"(st + 2 * L::PLANE + lane));
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(cv) : "r"(st + 2 * L::PLANE + kCaTile + lane));
+        cv = ok ? cv : 0u;
+        const int e_new = max(e_ref, (int)__reduce_max_sync(0xffffffffu, cv));
         if (e_new != e_ref) {
           const float f = e_ref == 0 ? 0.f : fast_exp2((float)(e_ref - e_new));
           e_ref = e_new;
@@ -403,21 +406,29 @@ __global__ void __launch_bounds__(kCaThreads, 1) cache_attend_kernel(const Cache
 #pragma unroll
               for (int k = 0; k < 4; ++k) o[m][d][k] *= f;
         }
+        // each lane makes its position's two factors, 2^e and 2^(e - E + 7); then a lane takes those of its 8 positions
+        const uint32_t fs = smem_u32(factors[warp]);
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(fs + 4 * lane), "r"(ck << 23) : "memory");
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(fs + 128 + 4 * lane), "r"((uint32_t)max((int)cv - e_ref + 134, 0) << 23)
+                     : "memory");
+        __syncwarp();
+        uint64_t kf[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+        for (int j = 0; j < NT; j += 2) {
+          const uint4 a = lds128(fs + 32 * t + 8 * j), b = lds128(fs + 128 + 32 * t + 8 * j);
+          kf[j] = f2pack(__uint_as_float(a.x), __uint_as_float(a.y));
+          kf[j + 1] = f2pack(__uint_as_float(a.z), __uint_as_float(a.w));
+          vf[j] = f2pack(__uint_as_float(b.x), __uint_as_float(b.y));
+          vf[j + 1] = f2pack(__uint_as_float(b.z), __uint_as_float(b.w));
+        }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int sh = 8 * ((2 * j + e) & 3);
-            const uint32_t ck = ((j < 2 ? kc.x : kc.y) >> sh) & 0xffu, cv = ((j < 2 ? vc.x : vc.y) >> sh) & 0xffu;
-            const float kf = __uint_as_float(ck << 23);
-            const int d = (int)cv - e_ref + 127 + 7;  // 2^(e - E + 7)
-            vf[2 * j + e] = __uint_as_float((uint32_t)(d < 0 ? 0 : min(d, 134)) << 23);
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              sc[m][j][e] *= kf * fac[m][0];
-              sc[m][j][2 + e] *= kf * fac[m][1];
-            }
-          }
+          for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+              f2unpack(fmul2(f2pack(sc[m][j][2 * hh], sc[m][j][2 * hh + 1]), fmul2(kf[j], f2pack(fac[m][hh], fac[m][hh]))),
+                       sc[m][j][2 * hh], sc[m][j][2 * hh + 1]);
       } else {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -475,14 +486,26 @@ __global__ void __launch_bounds__(kCaThreads, 1) cache_attend_kernel(const Cache
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           const float ref = mr[m][hh] == -INFINITY ? 0.f : mr[m][hh];
-          float sum = 0.f;
+          const uint64_t nr = f2pack(-ref, -ref);
+          uint64_t sum2 = f2pack(0.f, 0.f);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            const float w0 = fast_exp2(sc[m][j][2 * hh] - ref), w1 = fast_exp2(sc[m][j][2 * hh + 1] - ref);
-            sum += w0 + w1;
-            if constexpr (FP8) pf[m][j][hh] = pack_f16x2(w0 * vf[2 * j], w1 * vf[2 * j + 1]);
-            else pf[m][j][hh] = pack_bf16x2(w0, w1);
+            float w0, w1;
+            f2unpack(fadd2(f2pack(sc[m][j][2 * hh], sc[m][j][2 * hh + 1]), nr), w0, w1);
+            w0 = fast_exp2(w0);
+            w1 = fast_exp2(w1);
+            const uint64_t w = f2pack(w0, w1);
+            sum2 = fadd2(sum2, w);
+            if constexpr (FP8) {
+              f2unpack(fmul2(w, vf[j]), w0, w1);
+              pf[m][j][hh] = pack_f16x2(w0, w1);
+            } else {
+              pf[m][j][hh] = pack_bf16x2(w0, w1);
+            }
           }
+          float sum, sum1;
+          f2unpack(sum2, sum, sum1);
+          sum += sum1;
           l[m][hh] += sum;
         }
 
