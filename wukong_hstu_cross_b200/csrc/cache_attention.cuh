@@ -62,19 +62,23 @@ __device__ __forceinline__ void ca_write_cut(CaCut* c, int first_row, int row0, 
 __device__ __forceinline__ long long ca_slice_of(long long u, long long W, long long T) { return ((u + 1) * W - 1) / T; }
 
 constexpr int kCaTile = 32;     // positions of a unit
-constexpr int kCaWarps = 8;     // warps of a CTA (one CTA per SM)
-constexpr int kCaThreads = 32 * kCaWarps;
+// Warps of a CTA (one CTA per SM) for blocks of 16 mt rows. What is in flight is the same; the conversions of e4m3 fragments
+// leave gaps that more warps fill: 64 users, one row, d 512, histories of up to 15000 rows 121 us with 8 warps, 103 with
+// 12, 102 with 16. With 32 rows 12 warps have too few registers, and pairs of warps that share the tiles and
+// convert them twice take 178 us with 16 warps where 8 warps of 32 rows take 165.
+constexpr int ca_warps(bool fp8, int mt) { return fp8 && mt == 1 ? 12 : 8; }
 constexpr int kCaMinUnits = 4;  // a warp's least share, where there is little work: partials cost more than units
 constexpr float kCaLazy = 8.0f; // log2 headroom before the reference is raised
 
-template <int DH, bool FP8>
+template <int DH, bool FP8, int MT>
 struct CaTile {
   static constexpr int ROW = FP8 ? DH : 2 * DH;           // bytes of a row
   static constexpr int PLANE = kCaTile * ROW;
   static constexpr int SCALES = FP8 ? 2 * kCaTile : 0;    // K's, V's
   static constexpr int BYTES = 2 * PLANE + SCALES;
-  static constexpr int STAGES = 24576 / BYTES < 8 ? 24576 / BYTES : 8;
-  static constexpr int SMEM = kCaWarps * STAGES * BYTES;
+  static constexpr int SHARE = 196608 / ca_warps(FP8, MT);
+  static constexpr int STAGES = SHARE / BYTES < 8 ? SHARE / BYTES : 8;
+  static constexpr int SMEM = ca_warps(FP8, MT) * STAGES * BYTES;
   static_assert(STAGES >= 3 && BYTES % 16 == 0 && SMEM <= 220 * 1024, "ring");
   // byte offset of 16-byte chunk `ch` of row r: conflict-free for the fragment reads below
   static __device__ __forceinline__ int at(int r, int ch) {
@@ -144,8 +148,9 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 }
 
 template <int DH, bool FP8, int MT>
-__global__ void __launch_bounds__(kCaThreads, 1) cache_attend_kernel(const CacheAttnArgs p) {
-  using L = CaTile<DH, FP8>;
+__global__ void __launch_bounds__(32 * ca_warps(FP8, MT), 1) cache_attend_kernel(const CacheAttnArgs p) {
+  using L = CaTile<DH, FP8, MT>;
+  constexpr int kCaWarps = ca_warps(FP8, MT), kCaThreads = 32 * kCaWarps;
   constexpr int BM = 16 * MT, NT = kCaTile / 8, KS = DH / 16, ND = DH / 8, STAGES = L::STAGES;
   extern __shared__ __align__(128) uint8_t ring_all[];
   __shared__ long long sums[kCaThreads + 1];

@@ -2746,7 +2746,7 @@ whale_status plan_cache_attention(const Shape& s, const whale_cache& k, const wh
   // rows and positions are counted in 32 bits in the kernels
   if (c.total_new * s.h >= (1ll << 31) || c.max_length > (1 << 30)) return WHALE_ERR_UNSUPPORTED;
   p->n_qb = (int)std::max(1ll, cdiv<long long>(rows, p->bm));
-  const size_t slices = (size_t)kNumSM * (p->bm == kCpRows ? 1 : kCaWarps), slots = 2 * slices;
+  const size_t slices = (size_t)kNumSM * (p->bm == kCpRows ? 1 : ca_warps(k.format == WHALE_CACHE_E4M3, p->bm / 16)), slots = 2 * slices;
   p->ml_off = align_up(slots * p->bm * s.dh * 4);
   p->cuts_off = p->ml_off + align_up(slots * p->bm * 8);
   p->bytes = p->cuts_off + align_up(slices * sizeof(CaCut));
@@ -2756,10 +2756,10 @@ whale_status plan_cache_attention(const Shape& s, const whale_cache& k, const wh
 template <int DH, bool FP8, int MT>
 whale_status launch_attend_rows(const CacheAttnArgs& a, cudaStream_t st) {
   auto kern = cache_attend_kernel<DH, FP8, MT>;
-  constexpr int smem = CaTile<DH, FP8>::SMEM;
+  constexpr int smem = CaTile<DH, FP8, MT>::SMEM, warps = ca_warps(FP8, MT);
   CUCHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  WCHECK(launch_pdl(kern, dim3(kNumSM), dim3(kCaThreads), smem, st, a));
-  return launch_pdl(cache_attend_merge_kernel<DH, 16 * MT>, dim3(kNumSM * kCaWarps), dim3(kCaMergeThreads), 0, st, a);
+  WCHECK(launch_pdl(kern, dim3(kNumSM), dim3(32 * warps), smem, st, a));
+  return launch_pdl(cache_attend_merge_kernel<DH, 16 * MT>, dim3(kNumSM * warps), dim3(kCaMergeThreads), 0, st, a);
 }
 template <int DH, bool FP8>
 whale_status launch_attend(const CacheAttnPlan& p, const CacheAttnArgs& a, cudaStream_t st) {
