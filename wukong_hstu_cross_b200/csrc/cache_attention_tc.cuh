@@ -9,8 +9,9 @@
 // One CTA per SM takes a contiguous slice of the units (128 positions of one item = (sequence, K|V head, block of 256
 // rows)), all items' units laid end to end; causal items end at their last row's position. Partials where a slice cuts an
 // item, joined by cache_attend_merge_kernel in the order of the slices. Inside a CTA, for two tiles of 128 rows:
-//   warps 0-1   queries, and K and V of a unit, into 3 stages: bf16 by cp.async, e4m3 through registers, where
-//               number * 2^e becomes the bf16 number that it is. Rows in no page or past the end are zeros.
+//   warps 0-1   bf16: queries, and K and V of a unit, into stages by cp.async. e4m3: raw bytes by bulk copies, up to three
+//               units ahead, from which warps 12-15 make the bf16 number that number * 2^e is. Rows in no page or
+//               past the end are zeros.
 //   warps 2-3   a tile each: S = Q K^T (128 x 128, K = d_head) and O += P V (128 x d_head, K = 128)
 //   warps 4-11  one thread per row: scores out of tensor memory, running maximum (the reference is raised when the
 //               tile's maximum exceeds it by 2^8, with the rescale of O in tensor memory then), weights as bf16 back
@@ -23,25 +24,32 @@ namespace whale {
 
 constexpr int kCpRows = 256;     // rows of an item: two tiles
 constexpr int kCpUnit = 128;     // positions of a unit
-constexpr int kCpThreads = 384;       // three warpgroups, 168 registers a thread at launch
-// Registers afterwards: a row's 128 scores stay in a softmax thread's, a tile of raw e4m3 bytes in the producers'.
-constexpr int cp_regs_other(bool fp8) { return fp8 ? 120 : 88; }
-constexpr int cp_regs_softmax(bool fp8) { return fp8 ? 192 : 208; }
-static_assert(cp_regs_other(true) + 2 * cp_regs_softmax(true) <= 3 * 168 && cp_regs_other(false) + 2 * cp_regs_softmax(false) <= 3 * 168,
+// Three warpgroups for bf16 pages: loads and products, and two of softmax; a fourth that converts for e4m3 ones.
+constexpr int cp_threads(bool fp8) { return fp8 ? 512 : 384; }
+constexpr int cp_producers(bool fp8) { return fp8 ? 4 : 2; }  // warps that write the tiles
+// Registers after the start: a row's 128 scores stay in a softmax thread's. With what the block was launched with
+// (65536 / threads, a multiple of 8) they must add up, or the last one would wait for ever.
+constexpr int kCpRegsLoad = 88, kCpRegsSoftmax = 208;                               // bf16: 3 x 168
+constexpr int kCpRegsLoadE4m3 = 64, kCpRegsConvert = 96, kCpRegsSoftmaxE4m3 = 176;  // e4m3: 4 x 128
+static_assert(kCpRegsLoad + 2 * kCpRegsSoftmax <= 3 * 168 && kCpRegsLoadE4m3 + kCpRegsConvert + 2 * kCpRegsSoftmaxE4m3 <= 4 * 128,
               "the warpgroups share what the block was launched with");
-constexpr int kCpProducers = 64;
 constexpr int kCpMinUnits = 2;
 
-template <int DH>
+template <int DH, bool FP8>
 struct CpSmem {
   static constexpr int ROW = 2 * DH;                         // bytes of a row of Q, K, V
   static constexpr uint32_t TILE = 128 * ROW;                // 128 rows
-  static constexpr int ST = 4;
+  static constexpr int ST = FP8 ? 3 : 4;
+  static constexpr uint32_t RAW = FP8 ? 128 * DH : 0;         // raw e4m3 bytes of a plane
+  static constexpr uint32_t RAW_STAGE = FP8 ? 2 * RAW + 256 : 0;  // K, V, K's scales, V's
+  static constexpr int RST = 3;
   static constexpr int OFF_Q = 0;                            // [2 buffers][2 tiles]
   static constexpr int OFF_KV = OFF_Q + 4 * (int)TILE;       // [ST][K, V]
-  static constexpr int OFF_BAR = OFF_KV + ST * 2 * (int)TILE;
-  // kvfull[ST], kvempty[ST], qfree[2], sfull[2], sfree[2], pfull[2], pfree[2], tmem slot, abort flag
-  static constexpr size_t BYTES = 1024 + OFF_BAR + (2 * ST + 10) * 8 + 16;
+  static constexpr int OFF_RAW = OFF_KV + ST * 2 * (int)TILE;  // [RST]
+  static constexpr int OFF_BAR = OFF_RAW + RST * (int)RAW_STAGE;
+  // kvfull[ST], kvempty[ST], qfree[2], sfull[2], sfree[2], pfull[2], pfree[2], rawfull[RST], rawfree[RST], tmem slot, abort flags[2],
+  // which 16 rows of a raw stage are there [RST]
+  static constexpr size_t BYTES = 1024 + OFF_BAR + (2 * ST + 10 + 2 * RST) * 8 + 12 + 4 * RST;
   static_assert(BYTES <= 232448 - 1024, "shared memory of one CTA");
   // byte offset of 16-byte chunk ch of row r: the 128-byte (d_head 64) or 64-byte swizzle
   static __device__ __forceinline__ uint32_t at(int r, int ch) {
@@ -139,6 +147,7 @@ struct CpWalk {
     __syncwarp();
     int more = 0;
     if ((threadIdx.x & 31) == 0) more = step(p);
+    __syncwarp();
     return __shfl_sync(0xffffffffu, more, 0);
   }
 };
@@ -156,6 +165,13 @@ __device__ __forceinline__ uint4 cp_bf16x8(uint2 q, float f) {
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Bulk copy of `bytes` (a multiple of 16, as both addresses are) to shared memory, counted on `bar`.
+__device__ __forceinline__ void cp_bulk(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 
 // The MMAs of a whole warp, issued by one elected lane. _ts: A (M = 128 rows, 16 bf16 columns as 8 words a row)
@@ -194,8 +210,9 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 template <int DH, bool FP8>
-__global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __grid_constant__ CacheAttnArgs p) {
-  using L = CpSmem<DH>;
+__global__ void __launch_bounds__(cp_threads(FP8), 1) cache_attend_tc_kernel(const __grid_constant__ CacheAttnArgs p) {
+  using L = CpSmem<DH, FP8>;
+  constexpr int kCpThreads = cp_threads(FP8);
   constexpr int ST = L::ST;
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long sums[kCpThreads / 32 + 1];
@@ -207,13 +224,16 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
   uint64_t* sfree = sfull + 2;
   uint64_t* pfull = sfree + 2;
   uint64_t* pfree = pfull + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pfree + 2);
+  uint64_t* rawfull = pfree + 2;   // [RST] e4m3: raw bytes of a unit there, and read by both producers
+  uint64_t* rawfree = rawfull + L::RST;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rawfree + L::RST);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* pieces_of = reinterpret_cast<volatile uint32_t*>(tmem_slot + 3);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     for (int s = 0; s < ST; ++s) {
-      mbar_init(&kvfull[s], kCpProducers / 32);
+      mbar_init(&kvfull[s], cp_producers(FP8));
       mbar_init(&kvempty[s], 2);  // both tiles
     }
     for (int h = 0; h < 2; ++h) {
@@ -223,7 +243,11 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
       mbar_init(&pfull[h], 4);
       mbar_init(&pfree[h], 1);
     }
-    *abort_flag = 0;
+    for (int s = 0; s < L::RST; ++s) {
+      mbar_init(&rawfull[s], 1);
+      mbar_init(&rawfree[s], cp_producers(FP8));
+    }
+    abort_flag[0] = abort_flag[1] = 0;  // [1]: of the wait for copies in flight at the end
     fence_mbar_init();
     fence_proxy_async_smem();
   }
@@ -281,12 +305,31 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
   if (lane == 0 && u_lo < u_hi) walk.begin(p, start_b, start_at, u_lo, u_hi - u_lo);
   __syncwarp();
 
+  // A segment's queries into its buffer, the producers' warps each a part of the rows, by cp.async; and its bounds' errors.
+  auto queries = [&](int seg, int part) -> bool {
+    constexpr int CH = L::ROW / 16, RPI = 32 / CH, PARTS = cp_producers(FP8);
+    if (part == 0 && lane == 0 && p.c.lengths[walk.b] > walk.s.len) atomicOr(&g_device_error, kErrPages);
+    if (part == 0 && lane == 0 && walk.s.rows > walk.s.take) atomicOr(&g_device_error, kErrOffsets);
+    if (seg >= 2 && !warp_wait(&qfree[seg & 1], ((seg >> 1) - 1) & 1, abort_flag)) return false;
+    const uint32_t q_base = smem_u32(smem + L::OFF_Q) + (seg & 1) * 2 * L::TILE;
+#pragma unroll 4
+    for (int k = 0; k < kCpRows / PARTS / RPI; ++k) {
+      const int r = part * (kCpRows / PARTS) + k * RPI + lane / CH, ch = lane % CH;
+      const bool live = r < walk.n_rows;
+      const int row = walk.qb * kCpRows + (live ? r : 0), tok = row / p.group, head = walk.kvh * p.group + row % p.group;
+      cp_async16(q_base + (r >> 7) * L::TILE + L::at(r & 127, ch),
+                 p.q + (long long)(walk.s.first_row + tok) * p.ldq + head * DH + ch * 8, live ? 16u : 0u);
+    }
+    return true;
+  };
+
   if (u_lo >= u_hi) {  // no units: nothing but the common end
     if (tid == 0) ca_write_cut(p.cuts + blockIdx.x, 0, 0, 0, 0, 0, 0);
   } else if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(cp_regs_other(FP8)));
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FP8 ? kCpRegsLoadE4m3 : kCpRegsLoad));
     if (warp < 2) {
-    // ---------------- producers ----------------
+    if constexpr (!FP8) {
+    // ---------------- bf16: queries and tiles, 64 of a unit's positions a warp ----------------
     constexpr int CH = L::ROW / 16, RPI = 32 / CH;  // 16-byte chunks of a row, rows of a warp's instruction
     int n = 0, seg = 0;                             // tiles and segments so far
     bool ok = true;
@@ -294,8 +337,6 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
     do {
       const long long kv_off = (long long)walk.kvh << p.c.page_shift;
       const int t_lo = walk.t_lo, t_hi = walk.t_hi, len = walk.s.len, seq = walk.b;
-      if (tid == 0 && p.c.lengths[walk.b] > walk.s.len) atomicOr(&g_device_error, kErrPages);
-      if (tid == 0 && walk.s.rows > walk.s.take) atomicOr(&g_device_error, kErrOffsets);
       // rows (of each plane's first head) of this lane's two positions of unit i: the warp has 64 of the 128
       long long at[2];
       auto look = [&](int i) {
@@ -311,94 +352,80 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
         }
       };
       look(t_lo);
-      // queries into this segment's buffer
-      if (seg >= 2 && !warp_wait(&qfree[seg & 1], ((seg >> 1) - 1) & 1, abort_flag)) break;
-      const uint32_t q_base = smem_u32(smem + L::OFF_Q) + (seg & 1) * 2 * L::TILE;
-#pragma unroll 4
-      for (int k = 0; k < kCpRows / 2 / RPI; ++k) {
-        const int r = warp * (kCpRows / 2) + k * RPI + lane / CH, ch = lane % CH;
-        const bool live = r < walk.n_rows;
-        const int row = walk.qb * kCpRows + (live ? r : 0), tok = row / p.group, head = walk.kvh * p.group + row % p.group;
-        cp_async16(q_base + (r >> 7) * L::TILE + L::at(r & 127, ch),
-                   p.q + (long long)(walk.s.first_row + tok) * p.ldq + head * DH + ch * 8, live ? 16u : 0u);
-      }
-      if constexpr (!FP8) {
-        for (int i = t_lo; i < t_hi; ++i, ++n) {
-          if (n >= ST && !warp_wait(&kvempty[n % ST], (n / ST - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t st = smem_u32(smem + L::OFF_KV) + (n % ST) * 2 * L::TILE;
-          const long long a0 = at[0], a1 = at[1];
-          look(i + 1);
-#pragma unroll
-          for (int k = 0; k < 64 / RPI; ++k) {
-            const int r = k * RPI + lane / CH, ch = lane % CH;
-            const long long src = __shfl_sync(0xffffffffu, k * RPI < 32 ? a0 : a1, r & 31);
-            const uint8_t* a = p.pages + (src < 0 ? 0 : src) * L::ROW + ch * 16;
-            const uint32_t dst = st + L::at(warp * 64 + r, ch), bytes = src < 0 ? 0u : 16u;
-            cp_async16(dst, a, bytes);
-            cp_async16(dst + L::TILE, a + (src < 0 ? 0 : v_off * L::ROW), bytes);
-          }
-          cp_async_commit();
-          // handed on at once: waiting to fill the next stage first would tie this tile to the P V two tiles back
-          cp_async_wait<0>();
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&kvfull[n % ST]);
+      if (!queries(seg, warp)) break;
+      for (int i = t_lo; i < t_hi; ++i, ++n) {
+        if (n >= ST && !warp_wait(&kvempty[n % ST], (n / ST - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
         }
-      } else {
-        constexpr int RCH = DH / 16, RRPI = 32 / RCH, PASS = 64 / RRPI;  // raw rows are DH bytes
-        uint4 raw[2][PASS];
-        uint32_t sc[2][PASS];
-        auto load = [&]() {
+        const uint32_t st = smem_u32(smem + L::OFF_KV) + (n % ST) * 2 * L::TILE;
+        const long long a0 = at[0], a1 = at[1];
+        look(i + 1);
 #pragma unroll
-          for (int k = 0; k < PASS; ++k) {
-            const int r = k * RRPI + lane / RCH, ch = lane % RCH;
-            const long long src = __shfl_sync(0xffffffffu, k * RRPI < 32 ? at[0] : at[1], r & 31);
-#pragma unroll
-            for (int pl = 0; pl < 2; ++pl) {
-              raw[pl][k] = make_uint4(0u, 0u, 0u, 0u);
-              sc[pl][k] = 0u;
-              if (src >= 0) {
-                const long long row = src + pl * v_off;
-                raw[pl][k] = *reinterpret_cast<const uint4*>(p.pages + row * DH + ch * 16);
-                sc[pl][k] = p.scales[row];
-              }
-            }
-          }
-        };
-        load();
-        for (int i = t_lo; i < t_hi; ++i, ++n) {
-          look(i + 1);
-          if (n >= ST && !warp_wait(&kvempty[n % ST], (n / ST - 1) & 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t st = smem_u32(smem + L::OFF_KV) + (n % ST) * 2 * L::TILE;
-#pragma unroll
-          for (int k = 0; k < PASS; ++k) {
-            const int r = warp * 64 + k * RRPI + lane / RCH, ch = lane % RCH;
-#pragma unroll
-            for (int pl = 0; pl < 2; ++pl) {
-              const float f = __uint_as_float(sc[pl][k] << 23);
-              sts128(st + pl * L::TILE + L::at(r, 2 * ch), cp_bf16x8(make_uint2(raw[pl][k].x, raw[pl][k].y), f));
-              sts128(st + pl * L::TILE + L::at(r, 2 * ch + 1), cp_bf16x8(make_uint2(raw[pl][k].z, raw[pl][k].w), f));
-            }
-          }
-          if (i + 1 < t_hi) load();
-          if (i == t_lo) {  // the queries too
-            cp_async_commit();
-            cp_async_wait<0>();
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&kvfull[n % ST]);
+        for (int k = 0; k < 64 / RPI; ++k) {
+          const int r = k * RPI + lane / CH, ch = lane % CH;
+          const long long src = __shfl_sync(0xffffffffu, k * RPI < 32 ? a0 : a1, r & 31);
+          const uint8_t* a = p.pages + (src < 0 ? 0 : src) * L::ROW + ch * 16;
+          const uint32_t dst = st + L::at(warp * 64 + r, ch), bytes = src < 0 ? 0u : 16u;
+          cp_async16(dst, a, bytes);
+          cp_async16(dst + L::TILE, a + (src < 0 ? 0 : v_off * L::ROW), bytes);
         }
+        cp_async_commit();
+        // handed on at once: waiting to fill the next stage first would tie this tile to the P V two tiles back
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kvfull[n % ST]);
       }
       ++seg;
     } while (ok && walk.next(p));
     asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 0) {
+    // ---------------- e4m3: raw bytes by bulk copies, a lane per piece of a page's rows ----------------
+    const int rows = min(1 << p.c.page_shift, kCpUnit), pieces = kCpUnit / rows;  // 16 to 128 rows, 8 to 1 pieces
+    const long long v_off = p.c.planes == 2 ? (long long)p.c.kv_heads << p.c.page_shift : 0;
+    int n = 0;
+    bool ok = true;
+    do {
+      const long long kv_off = (long long)walk.kvh << p.c.page_shift;
+      auto look = [&](int t) -> long long {  // the cache's row where this lane's piece of unit t begins
+        const int pos = t * kCpUnit + lane * rows;
+        if (lane >= pieces || t >= walk.t_hi || pos >= walk.s.len) return -1;
+        const long long r = cache_row(p.c, walk.b, pos);
+        if (r < 0) atomicOr(&g_device_error, kErrPages);
+        return r;
+      };
+      long long at = look(walk.t_lo);
+      for (int t = walk.t_lo; t < walk.t_hi; ++t, ++n) {
+        const int s = n % L::RST;
+        if (n >= L::RST && !warp_wait(&rawfree[s], (n / L::RST - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const uint32_t have = __ballot_sync(0xffffffffu, at >= 0);
+        if (lane == 0) {
+          uint32_t bits = 0;  // of 16 rows each
+          for (int k = 0; k < pieces; ++k)
+            if (have >> k & 1) bits |= ((1u << (rows >> 4)) - 1) << (k * (rows >> 4));
+          pieces_of[s] = bits;
+          mbar_arrive_expect_tx(&rawfull[s], __popc(have) * rows * 2 * (DH + 1));
+        }
+        __syncwarp();
+        if (at >= 0) {
+          const uint32_t st = smem_u32(smem + L::OFF_RAW) + s * L::RAW_STAGE, r = lane * rows;
+          const long long k_row = at + kv_off, v_row = k_row + v_off;
+          cp_bulk(st + r * DH, p.pages + k_row * DH, rows * DH, &rawfull[s]);
+          cp_bulk(st + L::RAW + r * DH, p.pages + v_row * DH, rows * DH, &rawfull[s]);
+          cp_bulk(st + 2 * L::RAW + r, p.scales + k_row, rows, &rawfull[s]);
+          cp_bulk(st + 2 * L::RAW + 128 + r, p.scales + v_row, rows, &rawfull[s]);
+        }
+        at = look(t + 1);
+      }
+    } while (ok && walk.next(p));
+    // nothing may be in flight when the block ends, also where a wait ran out
+    for (int k = max(0, n - L::RST); k < n; ++k)
+      mbar_wait(&rawfull[k % L::RST], (k / L::RST) & 1, abort_flag + 1, 100000000ull);
+    }
     } else {
     // ---------------- MMA issuers: warp 2 + h for tile h ----------------
     // A unit's S as soon as the softmax warps have read the S before it, across segments too, then the P V of the
@@ -461,8 +488,66 @@ __global__ void __launch_bounds__(kCpThreads, 1) cache_attend_tc_kernel(const __
     } while (ok && walk.next(p));
     if (ok) flush();
     }
+  } else if (FP8 && warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCpRegsConvert));
+    // ---------------- e4m3: queries, and raw bytes to tiles, 32 of a unit's positions a warp ----------------
+    const int cw = warp - 12;
+    int n = 0, seg = 0;
+    bool ok = true;
+    do {
+      const int t_lo = walk.t_lo, t_hi = walk.t_hi, len = walk.s.len;
+      if (!queries(seg, cw)) break;
+      constexpr int RCH = DH / 16, RRPI = 32 / RCH, PASS = 32 / RRPI;  // raw rows are DH bytes
+      for (int i = t_lo; i < t_hi; ++i, ++n) {
+        if (!warp_wait(&rawfull[n % L::RST], (n / L::RST) & 1, abort_flag) ||
+            (n >= ST && !warp_wait(&kvempty[n % ST], (n / ST - 1) & 1, abort_flag))) {
+          ok = false;
+          break;
+        }
+        // rows past the end, and rows in no page, are zeros, whatever their raw bytes are
+        const uint32_t there = pieces_of[n % L::RST];
+        const int left = len - i * kCpUnit;
+        const uint8_t* const raw = smem + L::OFF_RAW + (n % L::RST) * L::RAW_STAGE;
+        const uint32_t st = smem_u32(smem + L::OFF_KV) + (n % ST) * 2 * L::TILE;
+#pragma unroll
+        for (int pl = 0; pl < 2; ++pl) {
+          uint4 w[PASS];
+          float f[PASS];
+#pragma unroll
+          for (int k = 0; k < PASS; ++k) {
+            const int r = cw * 32 + k * RRPI + lane / RCH;
+            w[k] = *reinterpret_cast<const uint4*>(raw + pl * L::RAW + (cw * 32 + k * RRPI) * DH + lane * 16);
+            const uint32_t code = raw[2 * L::RAW + pl * 128 + r];
+            if (r >= left || !(there >> (r >> 4) & 1)) {
+              w[k] = make_uint4(0u, 0u, 0u, 0u);
+              f[k] = 0.f;
+            } else {
+              f[k] = __uint_as_float(code << 23);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < PASS; ++k) {
+            const int r = cw * 32 + k * RRPI + lane / RCH, ch = lane % RCH;
+            sts128(st + pl * L::TILE + L::at(r, 2 * ch), cp_bf16x8(make_uint2(w[k].x, w[k].y), f[k]));
+            sts128(st + pl * L::TILE + L::at(r, 2 * ch + 1), cp_bf16x8(make_uint2(w[k].z, w[k].w), f[k]));
+          }
+        }
+        if (i == t_lo) {  // the queries too
+          cp_async_commit();
+          cp_async_wait<0>();
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&kvfull[n % ST]);
+          mbar_arrive(&rawfree[n % L::RST]);
+        }
+      }
+      ++seg;
+    } while (ok && walk.next(p));
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(cp_regs_softmax(FP8)));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FP8 ? kCpRegsSoftmaxE4m3 : kCpRegsSoftmax));
     // ---------------- softmax and output: one thread per row ----------------
     const int q4 = warp & 3, h = (warp - 4) >> 2, row = q4 * 32 + lane;
     const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;

@@ -2766,9 +2766,9 @@ whale_status launch_attend(const CacheAttnPlan& p, const CacheAttnArgs& a, cudaS
   if (p.bm == 16) return launch_attend_rows<DH, FP8, 1>(a, st);
   if (p.bm == 32) return launch_attend_rows<DH, FP8, 2>(a, st);
   auto kern = cache_attend_tc_kernel<DH, FP8>;
-  constexpr int smem = (int)CpSmem<DH>::BYTES;
+  constexpr int smem = (int)CpSmem<DH, FP8>::BYTES;
   CUCHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  WCHECK(launch_pdl(kern, dim3(kNumSM), dim3(kCpThreads), smem, st, a));
+  WCHECK(launch_pdl(kern, dim3(kNumSM), dim3(cp_threads(FP8)), smem, st, a));
   return launch_pdl(cache_attend_merge_kernel<DH, kCpRows>, dim3(kNumSM, kCpRows / kCaMergeRows), dim3(kCaMergeThreads), 0, st, a);
 }
 
