@@ -67,7 +67,8 @@ constexpr int kCaTile = 32;     // positions of a unit
 // 12, 102 with 16. With 32 rows 12 warps have too few registers, and pairs of warps that share the tiles and
 // convert them twice take 178 us with 16 warps where 8 warps of 32 rows take 165.
 constexpr int ca_warps(bool fp8, int mt) { return fp8 && mt == 1 ? 12 : 8; }
-constexpr int kCaMinUnits = 4;  // a warp's least share, where there is little work: partials cost more than units
+constexpr int kCaMinUnits = 2;  // a warp's least share where there is little work: 12.1 us for one row of 8 heads over
+                                // 5000 positions; with 4 the units take longer, with 1 the join does (12.9, 13.3 us)
 constexpr float kCaLazy = 8.0f; // log2 headroom before the reference is raised
 
 template <int DH, bool FP8, int MT>

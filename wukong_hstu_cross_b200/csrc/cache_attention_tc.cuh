@@ -47,8 +47,8 @@ struct CpSmem {
   static constexpr int OFF_KV = OFF_Q + 4 * (int)TILE;       // [ST][K, V]
   static constexpr int OFF_RAW = OFF_KV + ST * 2 * (int)TILE;  // [RST]
   static constexpr int OFF_BAR = OFF_RAW + RST * (int)RAW_STAGE;
-  // kvfull[ST], kvempty[ST], qfree[2], sfull[2], sfree[2], pfull[2], pfree[2], rawfull[RST], rawfree[RST], tmem slot, abort flags[2],
-  // which 16 rows of a raw stage are there [RST]
+  // kvfull[ST], kvempty[ST], qfree[2], sfull[2], sfree[2], pfull[2], pfree[2], rawfull[RST], rawfree[RST], tmem slot,
+  // abort flags[2], which 16 rows of a raw stage are there [RST]
   static constexpr size_t BYTES = 1024 + OFF_BAR + (2 * ST + 10 + 2 * RST) * 8 + 12 + 4 * RST;
   static_assert(BYTES <= 232448 - 1024, "shared memory of one CTA");
   // byte offset of 16-byte chunk ch of row r: the 128-byte (d_head 64) or 64-byte swizzle
@@ -328,165 +328,165 @@ __global__ void __launch_bounds__(cp_threads(FP8), 1) cache_attend_tc_kernel(con
   } else if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FP8 ? kCpRegsLoadE4m3 : kCpRegsLoad));
     if (warp < 2) {
-    if constexpr (!FP8) {
-    // ---------------- bf16: queries and tiles, 64 of a unit's positions a warp ----------------
-    constexpr int CH = L::ROW / 16, RPI = 32 / CH;  // 16-byte chunks of a row, rows of a warp's instruction
-    int n = 0, seg = 0;                             // tiles and segments so far
-    bool ok = true;
-    const long long v_off = p.c.planes == 2 ? (long long)p.c.kv_heads << p.c.page_shift : 0;
-    do {
-      const long long kv_off = (long long)walk.kvh << p.c.page_shift;
-      const int t_lo = walk.t_lo, t_hi = walk.t_hi, len = walk.s.len, seq = walk.b;
-      // rows (of each plane's first head) of this lane's two positions of unit i: the warp has 64 of the 128
-      long long at[2];
-      auto look = [&](int i) {
+      if constexpr (!FP8) {
+        // ---------------- bf16: queries and tiles, 64 of a unit's positions a warp ----------------
+        constexpr int CH = L::ROW / 16, RPI = 32 / CH;  // 16-byte chunks of a row, rows of a warp's instruction
+        int n = 0, seg = 0;                             // tiles and segments so far
+        bool ok = true;
+        const long long v_off = p.c.planes == 2 ? (long long)p.c.kv_heads << p.c.page_shift : 0;
+        do {
+          const long long kv_off = (long long)walk.kvh << p.c.page_shift;
+          const int t_lo = walk.t_lo, t_hi = walk.t_hi, len = walk.s.len, seq = walk.b;
+          // rows (of each plane's first head) of this lane's two positions of unit i: the warp has 64 of the 128
+          long long at[2];
+          auto look = [&](int i) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int pos = i * kCpUnit + warp * 64 + k * 32 + lane;
-          at[k] = -1;
-          if (i < t_hi && pos < len) {
-            const long long r = cache_row(p.c, seq, pos);
+            for (int k = 0; k < 2; ++k) {
+              const int pos = i * kCpUnit + warp * 64 + k * 32 + lane;
+              at[k] = -1;
+              if (i < t_hi && pos < len) {
+                const long long r = cache_row(p.c, seq, pos);
+                if (r < 0) atomicOr(&g_device_error, kErrPages);
+                else at[k] = r + kv_off;
+              }
+            }
+          };
+          look(t_lo);
+          if (!queries(seg, warp)) break;
+          for (int i = t_lo; i < t_hi; ++i, ++n) {
+            if (n >= ST && !warp_wait(&kvempty[n % ST], (n / ST - 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            const uint32_t st = smem_u32(smem + L::OFF_KV) + (n % ST) * 2 * L::TILE;
+            const long long a0 = at[0], a1 = at[1];
+            look(i + 1);
+#pragma unroll
+            for (int k = 0; k < 64 / RPI; ++k) {
+              const int r = k * RPI + lane / CH, ch = lane % CH;
+              const long long src = __shfl_sync(0xffffffffu, k * RPI < 32 ? a0 : a1, r & 31);
+              const uint8_t* a = p.pages + (src < 0 ? 0 : src) * L::ROW + ch * 16;
+              const uint32_t dst = st + L::at(warp * 64 + r, ch), bytes = src < 0 ? 0u : 16u;
+              cp_async16(dst, a, bytes);
+              cp_async16(dst + L::TILE, a + (src < 0 ? 0 : v_off * L::ROW), bytes);
+            }
+            cp_async_commit();
+            // handed on at once: waiting to fill the next stage first would tie this tile to the P V two tiles back
+            cp_async_wait<0>();
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kvfull[n % ST]);
+          }
+          ++seg;
+        } while (ok && walk.next(p));
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      } else if (warp == 0) {
+        // ---------------- e4m3: raw bytes by bulk copies, a lane per piece of a page's rows ----------------
+        const int rows = min(1 << p.c.page_shift, kCpUnit), pieces = kCpUnit / rows;  // 16 to 128 rows, 8 to 1 pieces
+        const long long v_off = p.c.planes == 2 ? (long long)p.c.kv_heads << p.c.page_shift : 0;
+        int n = 0;
+        bool ok = true;
+        do {
+          const long long kv_off = (long long)walk.kvh << p.c.page_shift;
+          auto look = [&](int t) -> long long {  // the cache's row where this lane's piece of unit t begins
+            const int pos = t * kCpUnit + lane * rows;
+            if (lane >= pieces || t >= walk.t_hi || pos >= walk.s.len) return -1;
+            const long long r = cache_row(p.c, walk.b, pos);
             if (r < 0) atomicOr(&g_device_error, kErrPages);
-            else at[k] = r + kv_off;
+            return r;
+          };
+          long long at = look(walk.t_lo);
+          for (int t = walk.t_lo; t < walk.t_hi; ++t, ++n) {
+            const int s = n % L::RST;
+            if (n >= L::RST && !warp_wait(&rawfree[s], (n / L::RST - 1) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            const uint32_t have = __ballot_sync(0xffffffffu, at >= 0);
+            if (lane == 0) {
+              uint32_t bits = 0;  // of 16 rows each
+              for (int k = 0; k < pieces; ++k)
+                if (have >> k & 1) bits |= ((1u << (rows >> 4)) - 1) << (k * (rows >> 4));
+              pieces_of[s] = bits;
+              mbar_arrive_expect_tx(&rawfull[s], __popc(have) * rows * 2 * (DH + 1));
+            }
+            __syncwarp();
+            if (at >= 0) {
+              const uint32_t st = smem_u32(smem + L::OFF_RAW) + s * L::RAW_STAGE, r = lane * rows;
+              const long long k_row = at + kv_off, v_row = k_row + v_off;
+              cp_bulk(st + r * DH, p.pages + k_row * DH, rows * DH, &rawfull[s]);
+              cp_bulk(st + L::RAW + r * DH, p.pages + v_row * DH, rows * DH, &rawfull[s]);
+              cp_bulk(st + 2 * L::RAW + r, p.scales + k_row, rows, &rawfull[s]);
+              cp_bulk(st + 2 * L::RAW + 128 + r, p.scales + v_row, rows, &rawfull[s]);
+            }
+            at = look(t + 1);
           }
-        }
-      };
-      look(t_lo);
-      if (!queries(seg, warp)) break;
-      for (int i = t_lo; i < t_hi; ++i, ++n) {
-        if (n >= ST && !warp_wait(&kvempty[n % ST], (n / ST - 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const uint32_t st = smem_u32(smem + L::OFF_KV) + (n % ST) * 2 * L::TILE;
-        const long long a0 = at[0], a1 = at[1];
-        look(i + 1);
-#pragma unroll
-        for (int k = 0; k < 64 / RPI; ++k) {
-          const int r = k * RPI + lane / CH, ch = lane % CH;
-          const long long src = __shfl_sync(0xffffffffu, k * RPI < 32 ? a0 : a1, r & 31);
-          const uint8_t* a = p.pages + (src < 0 ? 0 : src) * L::ROW + ch * 16;
-          const uint32_t dst = st + L::at(warp * 64 + r, ch), bytes = src < 0 ? 0u : 16u;
-          cp_async16(dst, a, bytes);
-          cp_async16(dst + L::TILE, a + (src < 0 ? 0 : v_off * L::ROW), bytes);
-        }
-        cp_async_commit();
-        // handed on at once: waiting to fill the next stage first would tie this tile to the P V two tiles back
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&kvfull[n % ST]);
+        } while (ok && walk.next(p));
+        // nothing may be in flight when the block ends, also where a wait ran out
+        for (int k = max(0, n - L::RST); k < n; ++k)
+          mbar_wait(&rawfull[k % L::RST], (k / L::RST) & 1, abort_flag + 1, 100000000ull);
       }
-      ++seg;
-    } while (ok && walk.next(p));
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == 0) {
-    // ---------------- e4m3: raw bytes by bulk copies, a lane per piece of a page's rows ----------------
-    const int rows = min(1 << p.c.page_shift, kCpUnit), pieces = kCpUnit / rows;  // 16 to 128 rows, 8 to 1 pieces
-    const long long v_off = p.c.planes == 2 ? (long long)p.c.kv_heads << p.c.page_shift : 0;
-    int n = 0;
-    bool ok = true;
-    do {
-      const long long kv_off = (long long)walk.kvh << p.c.page_shift;
-      auto look = [&](int t) -> long long {  // the cache's row where this lane's piece of unit t begins
-        const int pos = t * kCpUnit + lane * rows;
-        if (lane >= pieces || t >= walk.t_hi || pos >= walk.s.len) return -1;
-        const long long r = cache_row(p.c, walk.b, pos);
-        if (r < 0) atomicOr(&g_device_error, kErrPages);
-        return r;
-      };
-      long long at = look(walk.t_lo);
-      for (int t = walk.t_lo; t < walk.t_hi; ++t, ++n) {
-        const int s = n % L::RST;
-        if (n >= L::RST && !warp_wait(&rawfree[s], (n / L::RST - 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const uint32_t have = __ballot_sync(0xffffffffu, at >= 0);
-        if (lane == 0) {
-          uint32_t bits = 0;  // of 16 rows each
-          for (int k = 0; k < pieces; ++k)
-            if (have >> k & 1) bits |= ((1u << (rows >> 4)) - 1) << (k * (rows >> 4));
-          pieces_of[s] = bits;
-          mbar_arrive_expect_tx(&rawfull[s], __popc(have) * rows * 2 * (DH + 1));
-        }
-        __syncwarp();
-        if (at >= 0) {
-          const uint32_t st = smem_u32(smem + L::OFF_RAW) + s * L::RAW_STAGE, r = lane * rows;
-          const long long k_row = at + kv_off, v_row = k_row + v_off;
-          cp_bulk(st + r * DH, p.pages + k_row * DH, rows * DH, &rawfull[s]);
-          cp_bulk(st + L::RAW + r * DH, p.pages + v_row * DH, rows * DH, &rawfull[s]);
-          cp_bulk(st + 2 * L::RAW + r, p.scales + k_row, rows, &rawfull[s]);
-          cp_bulk(st + 2 * L::RAW + 128 + r, p.scales + v_row, rows, &rawfull[s]);
-        }
-        at = look(t + 1);
-      }
-    } while (ok && walk.next(p));
-    // nothing may be in flight when the block ends, also where a wait ran out
-    for (int k = max(0, n - L::RST); k < n; ++k)
-      mbar_wait(&rawfull[k % L::RST], (k / L::RST) & 1, abort_flag + 1, 100000000ull);
-    }
     } else {
-    // ---------------- MMA issuers: warp 2 + h for tile h ----------------
-    // A unit's S as soon as the softmax warps have read the S before it, across segments too, then the P V of the
-    // unit before. The whole warp runs this with one lane elected per instruction, so that descriptors are uniform.
-    constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128);
-    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DH) | kIdescBMnMajor;
-    const int h = warp - 2;
-    const uint32_t kv0 = smem_u32(smem + L::OFF_KV), q0 = smem_u32(smem + L::OFF_Q);
-    const uint32_t s_tm = tmem_base + h * 128, o_tm = tmem_base + 256 + h * 64, p_tm = tmem_base + 384 + h * 64;
-    int n = 0, seg = 0, c = 0;       // units, segments, and units that have this tile, so far
-    int late = -1;                   // unit whose P V is to come
-    bool late_first = false, ok = true;
-    auto flush = [&]() {
-      if (late < 0) return;
-      if (!warp_wait(&pfull[h], (c - 1) & 1, abort_flag)) {
-        ok = false;
-        return;
-      }
-      tc_fence_after();
-      const uint32_t v_base = kv0 + ((late % ST) * 2 + 1) * L::TILE;
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        umma_f16_ts(o_tm, p_tm + k * 8, L::desc(v_base + k * 16 * L::ROW), idesc_pv, !late_first || k > 0 ? 1u : 0u);
-      umma_commit_elect(&pfree[h]);
-      umma_commit_elect(&kvempty[late % ST]);
-      late = -1;
-    };
-    do {
-      const int blocks = walk.t_hi - walk.t_lo;
-      const bool active = walk.n_rows > 128 * h;
-      const uint32_t q_base = q0 + ((seg & 1) * 2 + h) * L::TILE;
-      for (int i = 0; i < blocks && ok; ++i, ++n) {
-        ok = warp_wait(&kvfull[n % ST], (n / ST) & 1, abort_flag);
-        if (!ok) break;
-        if (!active) {
-          flush();
-          if (lane == 0) {
-            mbar_arrive(&kvempty[n % ST]);
-            if (i == blocks - 1) mbar_arrive(&qfree[seg & 1]);
-          }
-          continue;
-        }
-        if (c > 0 && !warp_wait(&sfree[h], (c - 1) & 1, abort_flag)) {
+      // ---------------- MMA issuers: warp 2 + h for tile h ----------------
+      // A unit's S as soon as the softmax warps have read the S before it, across segments too, then the P V of the
+      // unit before. The whole warp runs this with one lane elected per instruction, so that descriptors are uniform.
+      constexpr uint32_t idesc_s = idesc_bf16_f32(128, 128);
+      constexpr uint32_t idesc_pv = idesc_bf16_f32(128, DH) | kIdescBMnMajor;
+      const int h = warp - 2;
+      const uint32_t kv0 = smem_u32(smem + L::OFF_KV), q0 = smem_u32(smem + L::OFF_Q);
+      const uint32_t s_tm = tmem_base + h * 128, o_tm = tmem_base + 256 + h * 64, p_tm = tmem_base + 384 + h * 64;
+      int n = 0, seg = 0, c = 0;       // units, segments, and units that have this tile, so far
+      int late = -1;                   // unit whose P V is to come
+      bool late_first = false, ok = true;
+      auto flush = [&]() {
+        if (late < 0) return;
+        if (!warp_wait(&pfull[h], (c - 1) & 1, abort_flag)) {
           ok = false;
-          break;
+          return;
         }
         tc_fence_after();
-        const uint32_t k_base = kv0 + (n % ST) * 2 * L::TILE;
+        const uint32_t v_base = kv0 + ((late % ST) * 2 + 1) * L::TILE;
 #pragma unroll
-        for (int k = 0; k < DH / 16; ++k)
-          umma_f16_elect(s_tm, L::desc(q_base + k * 32), L::desc(k_base + k * 32), idesc_s, k > 0 ? 1u : 0u);
-        umma_commit_elect(&sfull[h]);
-        if (i == blocks - 1) umma_commit_elect(&qfree[seg & 1]);
-        flush();
-        late = n;
-        late_first = i == 0;
-        ++c;
-      }
-      ++seg;
-    } while (ok && walk.next(p));
-    if (ok) flush();
+        for (int k = 0; k < 8; ++k)
+          umma_f16_ts(o_tm, p_tm + k * 8, L::desc(v_base + k * 16 * L::ROW), idesc_pv, !late_first || k > 0 ? 1u : 0u);
+        umma_commit_elect(&pfree[h]);
+        umma_commit_elect(&kvempty[late % ST]);
+        late = -1;
+      };
+      do {
+        const int blocks = walk.t_hi - walk.t_lo;
+        const bool active = walk.n_rows > 128 * h;
+        const uint32_t q_base = q0 + ((seg & 1) * 2 + h) * L::TILE;
+        for (int i = 0; i < blocks && ok; ++i, ++n) {
+          ok = warp_wait(&kvfull[n % ST], (n / ST) & 1, abort_flag);
+          if (!ok) break;
+          if (!active) {
+            flush();
+            if (lane == 0) {
+              mbar_arrive(&kvempty[n % ST]);
+              if (i == blocks - 1) mbar_arrive(&qfree[seg & 1]);
+            }
+            continue;
+          }
+          if (c > 0 && !warp_wait(&sfree[h], (c - 1) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t k_base = kv0 + (n % ST) * 2 * L::TILE;
+#pragma unroll
+          for (int k = 0; k < DH / 16; ++k)
+            umma_f16_elect(s_tm, L::desc(q_base + k * 32), L::desc(k_base + k * 32), idesc_s, k > 0 ? 1u : 0u);
+          umma_commit_elect(&sfull[h]);
+          if (i == blocks - 1) umma_commit_elect(&qfree[seg & 1]);
+          flush();
+          late = n;
+          late_first = i == 0;
+          ++c;
+        }
+        ++seg;
+      } while (ok && walk.next(p));
+      if (ok) flush();
     }
   } else if (FP8 && warp >= 12) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCpRegsConvert));
@@ -707,7 +707,8 @@ __global__ void __launch_bounds__(kCaMergeThreads) cache_attend_merge_kernel(con
   __shared__ float2 sml[kCaMergeThreads];
   pdl_wait();
   pdl_trigger();
-  const int4 c0 = reinterpret_cast<const int4*>(p.cuts + blockIdx.x)[0], c1 = reinterpret_cast<const int4*>(p.cuts + blockIdx.x)[1];
+  const int4* const cut = reinterpret_cast<const int4*>(p.cuts + blockIdx.x);
+  const int4 c0 = cut[0], c1 = cut[1];
   const int first_row = c0.x, head0 = c0.w, n = c1.x, slot0 = c1.y;
   const int row0 = blockIdx.y * kCaMergeRows, n_rows = min(kCaMergeRows, c0.z - row0);  // of the block
   if (n <= 1 || n_rows <= 0) return;
@@ -731,7 +732,7 @@ __global__ void __launch_bounds__(kCaMergeThreads) cache_attend_merge_kernel(con
     float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (v < vecs) {
-#pragma unroll 4
+#pragma unroll 8
       for (int k = grp; k < n; k += groups) {
         const long long slot = (long long)(k == 0 ? slot0 : 2 * ((int)blockIdx.x + k)) * BM + row0 + r;
         join(m, l, o, *reinterpret_cast<const float2*>(p.part_ml + slot * 2),

@@ -406,14 +406,16 @@ def whale_get_device_error(stream=None) -> int:
 # ------------------------------------------------------------------------------------------------
 # norm and rotation, cached histories: descriptors (each keeps its tensors alive) and entry points
 # ------------------------------------------------------------------------------------------------
-def _rows_of(name, t, dtypes, ndim=2):
+def _rows_of(name, t, dtypes, ndim=2, device=None):
     """Checks a tensor that the library reads as rows: innermost stride 1, on the current device. Returns it."""
-    import torch
     if t.dtype not in dtypes or t.dim() != ndim:
         raise ValueError(f"{name}: {ndim} dimensions of {' or '.join(map(str, dtypes))} expected, got {t.dim()} of {t.dtype}")
     if t.numel() > 0 and t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if device is None:
+        import torch
+        device = torch.cuda.current_device()
+    if t.get_device() != device:
         raise ValueError(f"{name}: on {t.device}, not on the current CUDA device")
     return t
 
@@ -547,12 +549,21 @@ def make_chunk(offsets, lengths, page_table, max_new, max_length, total_new) -> 
     return c
 
 
-def _packed(name, t, cfg, cache, chunk, width):
+def _stream_on(stream):
+    """(stream handle, current device): one look at the current stream gives both."""
+    import torch
+    if stream is None:
+        st = torch.cuda.current_stream()
+        return st.cuda_stream, st.device_index
+    return _stream(stream), None
+
+
+def _packed(name, t, cfg, cache, chunk, width, device):
     """A packed [total_new, width] bf16 tensor's row stride, and the cache's planes and d_head, checked."""
     import torch
     if isinstance(t, int) or t is None:
         return width
-    _rows_of(name, t, (torch.bfloat16,))
+    _rows_of(name, t, (torch.bfloat16,), 2, device)
     if t.shape[0] < chunk.total_new or t.shape[1] != width:
         raise ValueError(f"{name}: {tuple(t.shape)}, [{chunk.total_new}, {width}] expected")
     pages = getattr(cache, "_keepalive", (None,))[0]
@@ -576,9 +587,9 @@ def whale_cache_scales_size(cfg, cache) -> int:
 
 def whale_cache_append(cfg, cache, chunk, kv, stream=None, raw=False):
     """Write the chunk's K|V rows to the cache, in its format."""
-    ld = _packed("kv", kv, cfg, cache, chunk, _kv_width(cfg, cache))
-    st = _lib.whale_cache_append(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk), _ptr(kv), ld,
-                                 _stream(stream))
+    handle, device = _stream_on(stream)
+    ld = _packed("kv", kv, cfg, cache, chunk, _kv_width(cfg, cache), device)
+    st = _lib.whale_cache_append(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk), _ptr(kv), ld, handle)
     if raw:
         return st
     _check(st, "whale_cache_append")
@@ -586,9 +597,9 @@ def whale_cache_append(cfg, cache, chunk, kv, stream=None, raw=False):
 
 def whale_cache_read(cfg, cache, chunk, kv, stream=None, raw=False):
     """Read the chunk's K|V rows back from the cache, as bf16."""
-    ld = _packed("kv", kv, cfg, cache, chunk, _kv_width(cfg, cache))
-    st = _lib.whale_cache_read(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk), _ptr(kv), ld,
-                               _stream(stream))
+    handle, device = _stream_on(stream)
+    ld = _packed("kv", kv, cfg, cache, chunk, _kv_width(cfg, cache), device)
+    st = _lib.whale_cache_read(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk), _ptr(kv), ld, handle)
     if raw:
         return st
     _check(st, "whale_cache_read")
@@ -600,10 +611,10 @@ def whale_cache_attention_workspace_size(cfg, cache, chunk) -> int:
 
 def whale_cache_attention(cfg, cache, chunk, q, a, workspace, workspace_bytes=None, flags=0, stream=None, raw=False):
     """Attention of the chunk's rows q over the cached histories (flags: WHALE_ATTEND_CAUSAL) into a."""
-    ldq, lda = _packed("q", q, cfg, cache, chunk, cfg.d), _packed("a", a, cfg, cache, chunk, cfg.d)
+    handle, device = _stream_on(stream)
+    ldq, lda = _packed("q", q, cfg, cache, chunk, cfg.d, device), _packed("a", a, cfg, cache, chunk, cfg.d, device)
     st = _lib.whale_cache_attention(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk), _ptr(q), ldq, _ptr(a),
-                                    lda, int(flags), _ptr(workspace), _ws_bytes(workspace, workspace_bytes),
-                                    _stream(stream))
+                                    lda, int(flags), _ptr(workspace), _ws_bytes(workspace, workspace_bytes), handle)
     if raw:
         return st
     _check(st, "whale_cache_attention")
