@@ -362,7 +362,7 @@ typedef struct {
 
 /* The queries, or the keys, of one call. Rows of x and y are n_heads * d_head numbers of cfg->dtype, ld_*
  * elements apart (ld_* and the pointers multiples of 16 bytes), so the K half of K|V rows can be given in place.
- * y may be x itself with the same stride; otherwise they must not overlap. rows = 0: nothing to do, the
+ * y may be x itself with the same stride; otherwise they must not overlap (nor one part's y the other's x). rows = 0: nothing to do, the
  * pointers are not read. */
 typedef struct {
   const void* x;
@@ -373,8 +373,10 @@ typedef struct {
   int n_heads;          /* heads of these rows, >= 1 (K may have fewer than Q) */
 } whale_head_rows;
 
-/* q, k: host structs (device pointers inside); either may be null. One kernel for both. Sums and angles
- * are kept in fp32 and fp64 and rounded once, to cfg->dtype. d_head: 32 or 64 in bf16 mode, 8 .. 128 in fp32 mode. */
+/* q, k: host structs (device pointers inside); either may be null. One kernel for both. Sums are kept in fp32 and
+ * rounded once, to cfg->dtype; angles are reduced in 64-bit fixed point, exact to 2^-32 of a turn at any position;
+ * sines and cosines are off by 2^-20 at most in bf16 mode, and as accurate as fp32 holds them in fp32 mode.
+ * d_head: 32 or 64 in bf16 mode; 8, 16, 32, 64 or 128 in fp32 mode. */
 whale_status whale_norm_rotate(const whale_config* cfg, const whale_rotary* rotary, const whale_head_rows* q,
                                const whale_head_rows* k, whale_stream_t stream);
 
@@ -382,7 +384,8 @@ whale_status whale_norm_rotate(const whale_config* cfg, const whale_rotary* rota
  *   d_gain = sum over rows and heads of dn * x * r,   r = 1 / sqrt(mean(x^2) + eps)
  *   dx     = r * dn * gain - x * r^3 * mean(dn * gain * x)
  * dy and dx have type grad_dtype (WHALE_FP32, or WHALE_BF16 in bf16 mode); d_gain is fp32. dx and d_gain are
- * overwritten (dx may be dy itself with the same stride); d_gain of a part with no rows is 0. The sums of d_gain have a
+ * overwritten (dx may be dy itself with the same stride, and nothing else that is read); the two parts' d_gain are
+ * two buffers; d_gain of a part with no rows is 0. The sums of d_gain have a
  * fixed order: repeated calls agree bit for bit. dq (dk) is read where q (k) is given. Workspace: whale_norm_rotate_workspace_size. */
 typedef struct {
   const void* dy;
@@ -431,14 +434,15 @@ typedef struct {
  * Checks on the device: a position below 0 or at or past lengths' bound (max_length, table_stride * page_size), or a page outside
  * [0, n_pages), is in no page. Such rows are not written, read as zeros (attention sees zero keys and values
  * there; positions past the bound are not seen), and WHALE_DEVERR_PAGES is recorded. Rows of a packed
- * tensor past offsets[B] are neither read nor written. Cached rows past lengths[b] are never used, whatever they hold. */
+ * tensor past offsets[B] are neither used nor written. Cached rows past lengths[b] are never used, whatever they hold. */
 typedef struct {
   const int* offsets;    /* device int32 [B+1], ascending from 0 */
   const int* lengths;    /* device int32 [B] */
   const int* page_table; /* device int32 [B, table_stride] */
   int table_stride;
   int B;
-  int max_new;           /* host bound of every n_b */
+  int max_new;           /* host bound of every n_b: attention leaves rows beyond it as they are and records
+                            WHALE_DEVERR_OFFSETS; append and read do not look at it */
   int max_length;        /* host bound of every length */
   long long total_new;   /* rows of the packed tensor (>= offsets[B]) */
 } whale_chunk;
@@ -459,7 +463,10 @@ whale_status whale_cache_read(const whale_config* cfg, const whale_cache* cache,
 /* Eq. (4) over the cache: for every row i and head of the chunk, a_i = softmax(q_i K^T / sqrt(d_head)) V over its
  * sequence's cached positions, q and a [total_new, n_heads * d_head] bf16 with row strides ld_q, ld_a. flags: 0, or
  * WHALE_ATTEND_CAUSAL: a row sees positions up to its own, lengths[b] - n_b + i. A row that sees nothing
- * (an empty history, a negative position) gives 0. Softmax statistics and sums are fp32. Cached rows
+ * (an empty history, a negative position) gives 0. Softmax statistics and sums are fp32; the weights that multiply V
+ * are rounded to bf16, or on an e4m3 cache with up to 32 rows (max_new * n_heads / n_kv_heads) to f16. Results do not
+ * depend on timing: repeated calls agree bit for bit. a must not overlap q. Supported: max_length <= 2^30,
+ * total_new * n_heads < 2^31. Cached rows
  * within lengths[b] must be finite (a causal row's weights of later positions are 0, and 0 times an infinity
  * is a NaN). Workspace: whale_cache_attention_workspace_size bytes, 256-byte aligned; nothing in it needs to be set or kept
  * between calls. */

@@ -577,6 +577,81 @@ def test_graphs_that_share_a_workspace_and_another_stream():
             assert all(torch.equal(o, w) for o, w in zip(outs, want)), order
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [3, 20, 150])
+def test_rows_beyond_the_hosts_bound_stay(fmt, n):
+    """max_new below a sequence's rows: the rows beyond it are left as they are, and reported."""
+    rng = np.random.default_rng(n)
+    c = Cache(rng, [300, 40], [n, 2], 4, 4, 32, 16, fmt)
+    q = bf16_randn(rng, c.total, 128)
+    want = _attend(c, q, True)
+    a = torch.full_like(want, 7.0)
+    chunk = c.chunk(max_new=2)
+    W.whale_cache_attention(c.cfg, c.handle(), chunk, _gpu(q, "bf16"), a,
+                            _ws(W.whale_cache_attention_workspace_size(c.cfg, c.handle(), chunk)), flags=W.WHALE_ATTEND_CAUSAL)
+    torch.cuda.synchronize()
+    assert W.whale_get_device_error() == W.WHALE_DEVERR_OFFSETS
+    assert (a[2:n] == 7.0).all()
+    for rows in (slice(0, 2), slice(n, n + 2)):
+        ref, mag = _np(want[rows]), np.abs(c.values[0 if rows.start == 0 else 1][:, -1]).max()
+        _close(_np(a[rows]), ref, 2 * _attend_tol(ref, mag), "rows within the bound")
+
+
+def test_two_streams_at_once():
+    """Two calls in flight at once, each with its own workspace and output, over one cache."""
+    rng = np.random.default_rng(13)
+    for n in (1, 24, 140):
+        c = Cache(rng, [4000, 900], [n, n], 8, 8, 64, 64, "e4m3")
+        qs = [bf16_randn(rng, c.total, 512) for _ in range(2)]
+        want = [_attend(c, q, False) for q in qs]
+        qt = [_gpu(q, "bf16") for q in qs]
+        size = W.whale_cache_attention_workspace_size(c.cfg, c.handle(), c.chunk())
+        ws, out = [_ws(size) for _ in qs], [torch.zeros_like(w) for w in want]
+        chunk, streams = c.chunk(), [torch.cuda.Stream() for _ in qs]
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for s, q, o, w in zip(streams, qt, out, ws):
+                W.whale_cache_attention(c.cfg, c.handle(), chunk, q, o, w, stream=s)
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(out, want))
+
+
+def test_no_rows_at_all():
+    """Sequences without rows, a batch of none, and a cache of no pages."""
+    rng = np.random.default_rng(14)
+    c = Cache(rng, [50, 0, 7], [0, 0, 0], 4, 4, 32, 16, "bf16")
+    q = torch.full((5, 128), 3.0, device=DEV, dtype=torch.bfloat16)
+    kv, a = torch.full((5, 256), 3.0, device=DEV, dtype=torch.bfloat16), torch.full_like(q, 7.0)
+    before = c.bytes()[0]
+    for max_new in (0, 4, 200):
+        chunk = c.chunk(total_new=5, max_new=max_new)
+        W.whale_cache_attention(c.cfg, c.handle(), chunk, q, a, _ws(W.whale_cache_attention_workspace_size(c.cfg, c.handle(), chunk)))
+        W.whale_cache_append(c.cfg, c.handle(), chunk, kv)
+        W.whale_cache_read(c.cfg, c.handle(), chunk, kv)
+        torch.cuda.synchronize()
+        assert (a == 7.0).all() and (kv == 3.0).all() and torch.equal(before, c.bytes()[0])
+    # rows of an empty history, which has no page: attention gives zeros, and nothing is reported
+    none = W.make_cache(torch.empty(0, 2, 4, 16, 32, device=DEV, dtype=torch.bfloat16))
+    for n in (1, 200):
+        chunk = W.make_chunk(_int([0, n]), _int([0]), torch.empty(1, 0, device=DEV, dtype=torch.int32), n, 0, n)
+        q, a = torch.ones(n, 128, device=DEV, dtype=torch.bfloat16), torch.full((n, 128), 7.0, device=DEV, dtype=torch.bfloat16)
+        W.whale_cache_attention(c.cfg, none, chunk, q, a, _ws(W.whale_cache_attention_workspace_size(c.cfg, none, chunk)))
+        torch.cuda.synchronize()
+        assert not a.any()
+
+
+def test_many_sequences():
+    """More sequences than a block has threads, most of them without rows or history."""
+    rng = np.random.default_rng(15)
+    B = 1500
+    lengths = np.where(rng.random(B) < 0.3, rng.integers(1, 60, B), 0)
+    new = np.where(rng.random(B) < 0.4, rng.integers(0, 4, B), 0)
+    for fmt, scale in (("bf16", 1), ("e4m3", 20)):
+        c = Cache(rng, lengths, np.minimum(new * scale, 70), 2, 2, 32, 16, fmt)
+        q = bf16_randn(rng, c.total, 64)
+        _check_attend(c, q, _attend(c, q, False), False, rows=None if scale == 1 else np.array([0, 19, 59]))
+
+
 def test_tensors_must_fit_the_call():
     rng = np.random.default_rng(9)
     c = Cache(rng, [40], [3], 8, 8, 32, 16, "bf16")

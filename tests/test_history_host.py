@@ -124,6 +124,11 @@ def test_cache_refusals_and_sizes():
     def attend(a=FAKE, ld_a=256, flags=0, w=FAKE, n=need):
         return W._lib.whale_cache_attention(cfg, _cache(), _chunk(), FAKE, 256, a, ld_a, flags, w, n, 0)
 
+    big = lambda **kw: W.whale_cache_attention_workspace_size(cfg, _cache(), _chunk(**kw))  # noqa: E731
+    assert big(max_length=1 << 30, table_stride=1 << 20) > 0 and big(max_length=(1 << 30) + 1) == 0
+    assert big(total_new=(1 << 28) - 1, max_new=1) > 0 and big(total_new=1 << 28, max_new=1) == 0  # 8 heads
+    for kw in (dict(max_length=(1 << 30) + 1), dict(total_new=1 << 28)):
+        assert W._lib.whale_cache_attention(cfg, _cache(), _chunk(**kw), FAKE, 256, FAKE, 256, 0, FAKE, ws, 0) == UNSUPPORTED
     assert attend(a=None) == INVALID and attend(a=FAKE + 8) == INVALID and attend(ld_a=248) == INVALID
     assert attend(ld_a=257) == INVALID and attend(flags=2) == INVALID
     assert attend(w=None) == WORKSPACE and attend(n=need - 1) == WORKSPACE and attend(w=FAKE + 128) == WORKSPACE
