@@ -294,23 +294,24 @@ __global__ void __launch_bounds__(32 * ca_warps(FP8, MT), 1) cache_attend_kernel
       l[m][0] = l[m][1] = 0.f;
     }
 
-    // lane's row of tile i in the cache (this head's K plane), -1: none
     const long long kv_off = (long long)kvh << p.c.page_shift;
     const uint32_t vpl = p.c.planes == 2 ? L::PLANE : 0;  // V's plane of a stage (K's with shared K = V)
     const long long v_off = p.c.planes == 2 ? (long long)p.c.kv_heads << p.c.page_shift : 0;
     const long long v_bytes = v_off * L::ROW;
-    auto look = [&](int i) -> int {  // rows of the pool are numbered in 31 bits
+    // the page of this lane's position of tile i: only loaded here, and looked at a tile later
+    const int* const table = p.c.table + (long long)b * p.c.table_stride;
+    auto look = [&](int i) -> int {
       const int pos = i * kCaTile + lane;
-      if (i >= t_hi || pos >= s.len) return -1;
-      const long long r = cache_row(p.c, b, pos);
-      if (r < 0) {
-        atomicOr(&g_device_error, kErrPages);
-        return -1;
-      }
-      return (int)(r + kv_off);
+      return i < t_hi && pos < s.len ? table[pos >> p.c.page_shift] : 0;
     };
-    auto fetch = [&](int i, int row) {  // tile i, whose lane's row is `row`
+    auto fetch = [&](int i, int page) {
       if (i >= t_hi) return;
+      int row = -1;  // in the pool (this head's K plane), whose rows are numbered in 31 bits; -1: none
+      if (i * kCaTile + lane < s.len) {
+        row = (int)page_row(p.c, page, i * kCaTile + lane);
+        if (row < 0) atomicOr(&g_device_error, kErrPages);
+        else row += (int)kv_off;
+      }
       const uint32_t st = ring + (uint32_t)((i - t_lo) % STAGES) * L::BYTES;
       constexpr int CH = L::ROW / 16, RPI = 32 / CH;  // 16-byte chunks of a row, rows of one instruction
 #pragma unroll

@@ -46,11 +46,13 @@ WHALE_HD inline int chunk_seq(const ChunkView& c, long long row) {
 
 // Row of the cache's first plane and head, in units of rows: ((page * planes + plane) * heads + head) *
 // page_size + slot; -1 if the row is in no page (a position or page outside the cache).
-WHALE_HD inline long long cache_row(const ChunkView& c, int b, long long pos) {
-  if (pos < 0 || pos >= c.capacity) return -1;
-  const int page = c.table[(long long)b * c.table_stride + (pos >> c.page_shift)];
+WHALE_HD inline long long page_row(const ChunkView& c, int page, long long pos) {
   if ((unsigned)page >= (unsigned)c.n_pages) return -1;
   return (((long long)page * c.planes * c.kv_heads) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
+}
+WHALE_HD inline long long cache_row(const ChunkView& c, int b, long long pos) {
+  if (pos < 0 || pos >= c.capacity) return -1;
+  return page_row(c, c.table[(long long)b * c.table_stride + (pos >> c.page_shift)], pos);
 }
 
 // The scale's exponent of a row whose largest magnitude is amax (finite or infinite, no NaN).
