@@ -264,15 +264,16 @@ __global__ void __launch_bounds__(kNrThreads, kNrFwdBlocksPerSM) norm_rotate_ker
 }
 
 // The backward's ring: a thread brings its own pieces of kNrStages - 1 steps ahead into its own slots of shared memory by
-// cp.async (no other thread reads them, so no barrier either). 512 + 109605 rows, d 512, bf16: 67 us, 5.1 TB/s; with one
-// step ahead in registers 78 us; with a third block an SM, which spills, 85 us.
-constexpr int kNrStages = 4, kNrStepHeads = 2;
+// cp.async (no other thread reads them, so no barrier either). Small blocks, so that the registers hold 20 warps an SM
+// and not 16. 512 + 109605 rows, d 512, bf16: 61 us, 5.6 TB/s; with blocks of 256 threads 68 us; with one step
+// ahead in registers instead of the ring 78 us.
+constexpr int kNrBwdThreads = 128, kNrStages = 3, kNrStepHeads = 2;
 template <typename T, typename GT>
 struct NrRing {
   static constexpr int V = 16 / sizeof(T);
   static constexpr int ITEMS = kNrStepHeads * (1 + V * (int)sizeof(GT) / 16);  // 16-byte slots of a step
-  static constexpr int SMEM = kNrStages * ITEMS * kNrThreads * 16;
-  static constexpr int BLOCKS = sizeof(T) == 4 ? 3 : 2;  // resident at once
+  static constexpr int SMEM = kNrStages * ITEMS * kNrBwdThreads * 16;
+  static constexpr int BLOCKS = sizeof(T) == 4 ? 7 : (sizeof(GT) == 4 ? 4 : 5);  // resident at once: what registers and ring allow
 };
 inline int nr_backward_blocks_per_sm(bool bf16_rows, bool bf16_grads) {
   return !bf16_rows ? NrRing<float, float>::BLOCKS
@@ -288,7 +289,7 @@ template <typename T, int V, bool ADJ>
 __device__ __forceinline__ void nr_fetch(uint32_t slot, const T* p1, const T* p2) {
   if constexpr (V * sizeof(T) == 32) {
     nr_copy<16>(slot, p1);
-    nr_copy<16>(slot + 16 * kNrThreads, p2);
+    nr_copy<16>(slot + 16 * kNrBwdThreads, p2);
   } else if constexpr (ADJ) {
     nr_copy<16>(slot, p1);
   } else {
@@ -303,7 +304,7 @@ __device__ __forceinline__ NrRaw<T, V> nr_take(uint32_t slot) {
   for (int i = 0; i < V * (int)sizeof(T) / 16; ++i)
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r.w[4 * i]), "=r"(r.w[4 * i + 1]), "=r"(r.w[4 * i + 2]), "=r"(r.w[4 * i + 3])
-                 : "r"(slot + 16 * kNrThreads * i));
+                 : "r"(slot + 16 * kNrBwdThreads * i));
   return r;
 }
 
@@ -311,10 +312,10 @@ __device__ __forceinline__ NrRaw<T, V> nr_take(uint32_t slot) {
 // needs no atomics: the warps' sums meet in shared memory, the blocks' in norm_rotate_gain_kernel, each in a
 // fixed order).
 template <typename T, typename GT, int DH, bool ADJ>
-__global__ void __launch_bounds__(kNrThreads, NrRing<T, GT>::BLOCKS)
+__global__ void __launch_bounds__(kNrBwdThreads, NrRing<T, GT>::BLOCKS)
     norm_rotate_backward_kernel(const __grid_constant__ NrArgs a) {
   using R = NrRing<T, GT>;
-  constexpr int V = R::V, C = V / 2, LPH = DH / V, RPW = 32 / LPH, WARPS = kNrThreads / 32, HU = kNrStepHeads;
+  constexpr int V = R::V, C = V / 2, LPH = DH / V, RPW = 32 / LPH, WARPS = kNrBwdThreads / 32, HU = kNrStepHeads;
   constexpr int GI = V * (int)sizeof(GT) / 16;  // slots of a head's gradient piece
   extern __shared__ __align__(16) uint8_t nr_ring[];
   __shared__ float sums[WARPS][DH];
@@ -354,9 +355,9 @@ __global__ void __launch_bounds__(kNrThreads, NrRing<T, GT>::BLOCKS)
 #pragma unroll
       for (int u = 0; u < HU; ++u)
         if (f_h + u < heads) {
-          const uint32_t slot = st + u * (1 + GI) * 16 * kNrThreads;
+          const uint32_t slot = st + u * (1 + GI) * 16 * kNrBwdThreads;
           nr_fetch<T, V, ADJ>(slot, fx + u * DH, fx + u * DH + gap);
-          nr_fetch<GT, V, ADJ>(slot + 16 * kNrThreads, fdy + u * DH, fdy + u * DH + gap);
+          nr_fetch<GT, V, ADJ>(slot + 16 * kNrBwdThreads, fdy + u * DH, fdy + u * DH + gap);
         }
       f_h += HU;
       fx += HU * DH;
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kNrThreads, NrRing<T, GT>::BLOCKS)
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  constexpr uint32_t STAGE = R::ITEMS * 16 * kNrThreads;
+  constexpr uint32_t STAGE = R::ITEMS * 16 * kNrBwdThreads;
 #pragma unroll
   for (int i = 0; i < kNrStages - 1; ++i) fetch(ring + i * STAGE);
   int stage = 0;
@@ -392,10 +393,10 @@ __global__ void __launch_bounds__(kNrThreads, NrRing<T, GT>::BLOCKS)
 #pragma unroll
       for (int u = 0; u < HU; ++u) {
         if (h0 + u < heads) {
-          const uint32_t slot = st + u * (1 + GI) * 16 * kNrThreads;
+          const uint32_t slot = st + u * (1 + GI) * 16 * kNrBwdThreads;
           float f[V], d[V], dn[V], e[V];
           nr_unpack<T, V, ADJ>(nr_take<T, V>(slot), f);
-          nr_unpack<GT, V, ADJ>(nr_take<GT, V>(slot + 16 * kNrThreads), d);
+          nr_unpack<GT, V, ADJ>(nr_take<GT, V>(slot + 16 * kNrBwdThreads), d);
 #pragma unroll
           for (int k = 0; k < C; k += 2) {
             const uint64_t da = f2pack(d[k], d[k + 1]), db = f2pack(d[C + k], d[C + k + 1]);
@@ -430,7 +431,7 @@ __global__ void __launch_bounds__(kNrThreads, NrRing<T, GT>::BLOCKS)
     if (lane < LPH) sums[warp][nr_col<V, ADJ>(l, k)] = dg[k];
   }
   __syncthreads();
-  for (int col = threadIdx.x; col < DH; col += kNrThreads) {
+  for (int col = threadIdx.x; col < DH; col += kNrBwdThreads) {
     float t = 0.f;
 #pragma unroll
     for (int w = 0; w < WARPS; ++w) t += sums[w][col];

@@ -2643,12 +2643,12 @@ void nr_turns(const Shape& s, const whale_rotary& r, NrArgs* a) {
   for (int i = 0; i < r.rotary_dim / 2; ++i, turns *= ratio) a->turns[i] = nr_turn_fraction(turns);
 }
 
-inline long long nr_blocks(const Shape& s, long long rows) {
-  return cdiv<long long>(rows, kNrThreads / (s.dh / (s.bf16 ? 8 : 4)));
+inline long long nr_blocks(const Shape& s, int threads, long long rows) {
+  return cdiv<long long>(rows, threads / (s.dh / (s.bf16 ? 8 : 4)));
 }
 // Blocks of the two parts: as many as there are rows for, up to `cap` in all, in proportion to the rows.
-inline void nr_split(const Shape& s, long long cap, long long rows0, long long rows1, int* b0, int* b1) {
-  const long long n0 = nr_blocks(s, rows0), n1 = nr_blocks(s, rows1);
+inline void nr_split(const Shape& s, int threads, long long cap, long long rows0, long long rows1, int* b0, int* b1) {
+  const long long n0 = nr_blocks(s, threads, rows0), n1 = nr_blocks(s, threads, rows1);
   cap = std::min(cap, n0 + n1);
   *b0 = n0 == 0 ? 0 : (int)std::max(1ll, std::min(n0, cap * n0 / (n0 + n1)));
   *b1 = n1 == 0 ? 0 : (int)std::max(1ll, std::min(n1, cap - *b0));
@@ -2670,7 +2670,7 @@ whale_status launch_norm_rotate_backward(bool adj, const NrArgs& a, unsigned gri
   auto kern = adj ? norm_rotate_backward_kernel<T, GT, DH, true> : norm_rotate_backward_kernel<T, GT, DH, false>;
   constexpr int smem = NrRing<T, GT>::SMEM;
   CUCHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  return launch_pdl(kern, dim3(grid), dim3(kNrThreads), smem, st, a);
+  return launch_pdl(kern, dim3(grid), dim3(kNrBwdThreads), smem, st, a);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -2810,7 +2810,7 @@ whale_status whale_norm_rotate(const whale_config* cfg, const whale_rotary* rota
   WCHECK(head_rows(s, q, nullptr, 0, &a.part[0]));
   WCHECK(head_rows(s, k, nullptr, 0, &a.part[1]));
   int b0, b1;
-  nr_split(s, kNrFwdBlocks, a.part[0].rows, a.part[1].rows, &b0, &b1);
+  nr_split(s, kNrThreads, kNrFwdBlocks, a.part[0].rows, a.part[1].rows, &b0, &b1);
   if (b0 + b1 == 0) return WHALE_OK;
   a.blocks0 = b0;
   nr_turns(s, *rotary, &a);
@@ -2832,7 +2832,7 @@ whale_status whale_norm_rotate(const whale_config* cfg, const whale_rotary* rota
 size_t whale_norm_rotate_workspace_size(const whale_config* cfg, const whale_head_rows* q, const whale_head_rows* k) {
   Shape s;
   if (validate(cfg, &s) != WHALE_OK || (q && q->rows < 0) || (k && k->rows < 0)) return 0;
-  return align_up((size_t)(4 * kNumSM) * s.dh * 4);
+  return align_up((size_t)(8 * kNumSM) * s.dh * 4);
 }
 
 whale_status whale_norm_rotate_backward(const whale_config* cfg, const whale_rotary* rotary, const whale_head_rows* q,
@@ -2854,7 +2854,7 @@ whale_status whale_norm_rotate_backward(const whale_config* cfg, const whale_rot
   if (!ws || ws_bytes < whale_norm_rotate_workspace_size(cfg, q, k) || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)))
     return WHALE_ERR_WORKSPACE;
   int b0, b1;
-  nr_split(s, nr_bwd_grid(s, grad_dtype), a.part[0].rows, a.part[1].rows, &b0, &b1);
+  nr_split(s, kNrBwdThreads, nr_bwd_grid(s, grad_dtype), a.part[0].rows, a.part[1].rows, &b0, &b1);
   a.blocks0 = b0;
   a.partial = static_cast<float*>(ws);
   nr_turns(s, *rotary, &a);
