@@ -640,6 +640,24 @@ def test_no_rows_at_all():
         assert not a.any()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("h,hk", [(8, 8), (8, 2)])
+def test_mixed_batch(fmt, h, hk):
+    """Many sequences with a few rows beside one with many: each kind is taken by its own kernel."""
+    rng = np.random.default_rng(h + hk)
+    for long, short in ((140, 1), (300, 5), (90, 4)):
+        B = 40
+        lengths, new = rng.integers(1, 400, B), np.minimum(rng.integers(0, short + 1, B), 8)
+        lengths[17], new[17] = 700, long
+        lengths[3], new[3] = 0, 1
+        c = Cache(rng, lengths, new, h, hk, 32, 32, fmt)
+        q = bf16_randn(rng, c.total, h * 32)
+        for causal in (False, True):
+            a = _attend(c, q, causal)
+            _check_attend(c, q, a, causal, rows=np.arange(0, 300, 13))
+            assert torch.equal(a, _attend(c, q, causal))
+
+
 def test_many_sequences():
     """More sequences than a block has threads, most of them without rows or history."""
     rng = np.random.default_rng(15)

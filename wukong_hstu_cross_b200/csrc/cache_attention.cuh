@@ -6,6 +6,7 @@
 // sequence and K|V head share every cached row: row r is token r / group, head kvh * group + r % group.
 //
 // Bound: HBM (each cached row is read once; 2 * n_b * group operations per byte of bf16).
+// 64 users, d 512, histories of up to 15000 rows: one row 139 us (bf16, 6.2 TB/s) and 101 us (e4m3), 32 rows 160 and 165 us.
 //
 // Split. Units of kCaTile positions of one (sequence, K|V head, block of BM rows) are laid end to end, and warp w of
 // W takes the contiguous slice [w T / W, (w + 1) T / W): every warp streams the same number of bytes whatever the
@@ -39,9 +40,9 @@ struct CacheAttnArgs {
   long long ldq, lda;
   const uint8_t* pages;
   const uint8_t* scales;
-  int heads, group, causal;
+  int group, causal;       // query heads of a K|V head
   int max_new;             // rows of a sequence, at most
-  int n_qb;                // row blocks of a sequence, at most
+  int rows_lo, rows_hi;    // this kernel's sequences: more than rows_lo rows x group, at most rows_hi
   float scale_log2;        // log2(e) / sqrt(d_head)
   float* part_o;           // [2 W, BM, DH]
   float* part_ml;          // [2 W, BM, 2]
@@ -104,7 +105,8 @@ __device__ __forceinline__ CaSeq ca_seq(const CacheAttnArgs& p, int b, int bm) {
   const long long n = p.c.lengths[b];
   s.len = (int)(n < 0 ? 0 : (n > p.c.capacity ? p.c.capacity : n));
   s.units = s.len <= kCaTile ? 1 : (s.len + kCaTile - 1) / kCaTile;
-  s.blocks = s.take <= 0 ? 0 : (s.take * p.group + bm - 1) / bm;
+  const int rows = max(s.take, 0) * p.group;
+  s.blocks = rows > p.rows_lo && rows <= p.rows_hi ? (rows + bm - 1) / bm : 0;
   return s;
 }
 __device__ __forceinline__ long long ca_units(const CacheAttnArgs& p, int b, int bm) {

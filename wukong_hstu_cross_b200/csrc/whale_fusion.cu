@@ -2735,20 +2735,30 @@ whale_status launch_rows(bool append, RowsArgs a, cudaStream_t st) {
 
 // Row blocks and workspace of the attention over the cache.
 struct CacheAttnPlan {
-  int bm, n_qb, max_new;
+  int bm, max_new;
+  int few;  // sequences of up to this many rows (x group) are taken from the tcgen05 kernel by the warp-level one (0: none)
   size_t ml_off, cuts_off, bytes;
 };
 whale_status plan_cache_attention(const Shape& s, const whale_cache& k, const whale_chunk& c, CacheAttnPlan* p) {
   const int group = s.h / k.n_kv_heads;
   p->max_new = (int)std::min<long long>(c.max_new, c.total_new);
-  const long long rows = (long long)p->max_new * group;
+  const long long rows = (long long)p->max_new * group, all = c.total_new * group;
   p->bm = rows <= 16 ? 16 : (rows <= 32 ? 32 : kCpRows);
+  // A batch whose average sequence is in the warp-level kernel's range while the longest is not (63 users with one new event
+  // and one with 1000, d 512: 169 us where the tcgen05 kernel alone takes 313): each kernel takes its own, one after
+  // the other in the same workspace.
+  p->few = p->bm != kCpRows ? 0 : (all <= 16ll * c.B ? 16 : (all <= 32ll * c.B ? 32 : 0));
   // rows and positions are counted in 32 bits in the kernels
   if (c.total_new * s.h >= (1ll << 31) || c.max_length > (1 << 30)) return WHALE_ERR_UNSUPPORTED;
-  p->n_qb = (int)std::max(1ll, cdiv<long long>(rows, p->bm));
-  const size_t slices = (size_t)kNumSM * (p->bm == kCpRows ? 1 : ca_warps(k.format == WHALE_CACHE_E4M3, p->bm / 16)), slots = 2 * slices;
-  p->ml_off = align_up(slots * p->bm * s.dh * 4);
-  p->cuts_off = p->ml_off + align_up(slots * p->bm * 8);
+  size_t slices = 0, rows_in_slots = 0;
+  for (int bm : {16, 32, kCpRows}) {
+    if (bm != p->bm && bm != p->few) continue;
+    const size_t n = (size_t)kNumSM * (bm == kCpRows ? 1 : ca_warps(k.format == WHALE_CACHE_E4M3, bm / 16));
+    slices = std::max(slices, n);
+    rows_in_slots = std::max(rows_in_slots, 2 * n * bm);
+  }
+  p->ml_off = align_up(rows_in_slots * s.dh * 4);
+  p->cuts_off = p->ml_off + align_up(rows_in_slots * 8);
   p->bytes = p->cuts_off + align_up(slices * sizeof(CaCut));
   return WHALE_OK;
 }
@@ -2765,11 +2775,17 @@ template <int DH, bool FP8>
 whale_status launch_attend(const CacheAttnPlan& p, const CacheAttnArgs& a, cudaStream_t st) {
   if (p.bm == 16) return launch_attend_rows<DH, FP8, 1>(a, st);
   if (p.bm == 32) return launch_attend_rows<DH, FP8, 2>(a, st);
+  CacheAttnArgs many = a;
+  many.rows_lo = p.few;
   auto kern = cache_attend_tc_kernel<DH, FP8>;
   constexpr int smem = (int)CpSmem<DH, FP8>::BYTES;
   CUCHECK(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-  WCHECK(launch_pdl(kern, dim3(kNumSM), dim3(cp_threads(FP8)), smem, st, a));
-  return launch_pdl(cache_attend_merge_kernel<DH, kCpRows>, dim3(kNumSM, kCpRows / kCaMergeRows), dim3(kCaMergeThreads), 0, st, a);
+  WCHECK(launch_pdl(kern, dim3(kNumSM), dim3(cp_threads(FP8)), smem, st, many));
+  WCHECK(launch_pdl(cache_attend_merge_kernel<DH, kCpRows>, dim3(kNumSM, kCpRows / kCaMergeRows), dim3(kCaMergeThreads), 0, st, many));
+  if (!p.few) return WHALE_OK;
+  CacheAttnArgs few = a;
+  few.rows_hi = p.few;
+  return p.few == 16 ? launch_attend_rows<DH, FP8, 1>(few, st) : launch_attend_rows<DH, FP8, 2>(few, st);
 }
 
 whale_status cache_rows_call(const whale_config* cfg, const whale_cache* cache, const whale_chunk* chunk,
@@ -2942,11 +2958,11 @@ whale_status whale_cache_attention(const whale_config* cfg, const whale_cache* c
   p.lda = ld_a;
   p.pages = static_cast<const uint8_t*>(cache->pages);
   p.scales = cache->scales;
-  p.heads = s.h;
   p.group = s.h / cache->n_kv_heads;
   p.causal = flags & WHALE_ATTEND_CAUSAL ? 1 : 0;
   p.max_new = plan.max_new;
-  p.n_qb = plan.n_qb;
+  p.rows_lo = 0;
+  p.rows_hi = 0x7fffffff;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)s.dh));
   p.part_o = static_cast<float*>(ws);
   p.part_ml = p.part_o + plan.ml_off / 4;
