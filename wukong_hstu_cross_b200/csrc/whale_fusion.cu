@@ -2744,9 +2744,9 @@ whale_status plan_cache_attention(const Shape& s, const whale_cache& k, const wh
   p->max_new = (int)std::min<long long>(c.max_new, c.total_new);
   const long long rows = (long long)p->max_new * group, all = c.total_new * group;
   p->bm = rows <= 16 ? 16 : (rows <= 32 ? 32 : kCpRows);
-  // A batch whose average sequence is in the warp-level kernel's range while the longest is not (63 users with one new event
-  // and one with 1000, d 512: 169 us where the tcgen05 kernel alone takes 313): each kernel takes its own, one after
-  // the other in the same workspace.
+  // A batch whose average sequence is in the warp-level kernel's range while the longest is not: each kernel takes its
+  // own, one after the other in the same workspace. 63 users with one new event and one with 200 (with 1000), d 512,
+  // histories of up to 15000 rows: 178 us (198) where the tcgen05 kernel alone takes 318 (342); e4m3 136 (207) and 367 (405).
   p->few = p->bm != kCpRows ? 0 : (all <= 16ll * c.B ? 16 : (all <= 32ll * c.B ? 32 : 0));
   // rows and positions are counted in 32 bits in the kernels
   if (c.total_new * s.h >= (1ll << 31) || c.max_length > (1 << 30)) return WHALE_ERR_UNSUPPORTED;
