@@ -232,3 +232,52 @@ def test_index_and_scale_arithmetic(tmp_path):
             assert int(e) == H.E_HI
         else:
             assert int(e) == int(H.quantise(np.array([[np.float32(a)]]))[1][0]), line
+
+
+CUTS = r"""
+#include <cstdio>
+#include "chunk_index.h"
+using namespace whale;
+
+int main() {
+  unsigned seed = 7;
+  auto rnd = [&](int n) { seed = seed * 1664525u + 1013904223u; return (int)((seed >> 8) % (unsigned)n); };
+  const int far[] = {-2147483647 - 1, -1, 0, 1, 2147483647};
+  auto any = [&](int n) { return rnd(4) ? rnd(n) : far[rnd(5)]; };  // what memory may hold
+  long long good = 0, bad = 0;
+  for (int t = 0; t < 3000000; ++t) {
+    ChunkView c{};
+    const int group = 1 + rnd(4), bm = rnd(2) ? 16 : 256, slices = 1 + rnd(40), slice = rnd(slices);
+    c.kv_heads = 1 + rnd(3);
+    c.total = rnd(60);
+    const int first_row = any(60), row0 = any(80), n_rows = any(20), head0 = any(12), parts = any(40);
+    const int slot = rnd(2) ? 2 * slice + rnd(2) : any(80);
+    if (!cut_valid(c, group, bm, slices, slice, first_row, row0, n_rows, head0, parts, slot)) { ++bad; continue; }
+    ++good;
+    for (int k = 0; k < parts; ++k) {
+      const int s = k == 0 ? slot : 2 * (slice + k);
+      if (s < 0 || s >= 2 * slices) return printf("slot %d of %d slices\n", s, slices), 1;
+    }
+    if (n_rows < 1 || n_rows > bm) return printf("rows\n"), 1;
+    for (int r = row0; r < row0 + n_rows; ++r) {
+      const long long row = (long long)first_row + r / group;
+      const int head = head0 + r % group;
+      if (r < 0 || row < 0 || row >= c.total || head < 0 || head >= c.kv_heads * group) return printf("row %lld head %d\n", row, head), 1;
+    }
+  }
+  // one that a slice leaves: 3 slices, rows 4 .. 6 of a sequence at row 10
+  ChunkView c{};
+  c.kv_heads = 2;
+  c.total = 14;
+  if (!cut_valid(c, 2, 16, 5, 1, 10, 4, 3, 2, 3, 3) || cut_valid(c, 2, 16, 5, 1, 0, 0, 0, 0, 0, 0)) return printf("cut\n"), 1;
+  if (good < 1000 || bad < 1000) return printf("coverage %lld %lld\n", good, bad), 1;
+  return 0;
+}
+"""
+
+
+def test_a_join_takes_only_cuts_in_range(tmp_path):
+    """A slice whose wait ran out leaves no word of its item; whatever the workspace then holds, the join of the partials
+    forms no index outside them or the rows."""
+    _run(tmp_path, "cuts.cpp", "g++", ["-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover",
+                                       "-I", os.path.join(ROOT, "wukong_hstu_cross_b200", "csrc")], CUTS)

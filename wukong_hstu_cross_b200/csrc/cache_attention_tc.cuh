@@ -301,6 +301,8 @@ __global__ void __launch_bounds__(cp_threads(FP8), 1) cache_attend_tc_kernel(con
       at += n;
     }
   }
+  // nothing to join, until the slice's last segment says otherwise: a wait that runs out ends the slice before that
+  if (tid == 0) ca_write_cut(p.cuts + blockIdx.x, 0, 0, 0, 0, 0, 0);
   __syncthreads();
   CpWalk& walk = walks[warp];
   if (lane == 0 && u_lo < u_hi) walk.begin(p, start_b, start_at, u_lo, u_hi - u_lo);
@@ -325,7 +327,6 @@ __global__ void __launch_bounds__(cp_threads(FP8), 1) cache_attend_tc_kernel(con
   };
 
   if (u_lo >= u_hi) {  // no units: nothing but the common end
-    if (tid == 0) ca_write_cut(p.cuts + blockIdx.x, 0, 0, 0, 0, 0, 0);
   } else if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FP8 ? kCpRegsLoadE4m3 : kCpRegsLoad));
     if (warp < 2) {
@@ -712,7 +713,7 @@ __global__ void __launch_bounds__(kCaMergeThreads) cache_attend_merge_kernel(con
   const int4 c0 = cut[0], c1 = cut[1];
   const int first_row = c0.x, head0 = c0.w, n = c1.x, slot0 = c1.y;
   const int row0 = blockIdx.y * kCaMergeRows, n_rows = min(kCaMergeRows, c0.z - row0);  // of the block
-  if (n <= 1 || n_rows <= 0) return;
+  if (n_rows <= 0 || !cut_valid(p.c, p.group, BM, gridDim.x, blockIdx.x, first_row, c0.y, c0.z, head0, n, slot0)) return;
   const int vecs = n_rows * (DH / 4);
   // `groups` threads take every groups-th partial of one vector of 4 columns
   int groups = 1;

@@ -55,6 +55,16 @@ WHALE_HD inline long long cache_row(const ChunkView& c, int b, long long pos) {
   return page_row(c, c.table[(long long)b * c.table_stride + (pos >> c.page_shift)], pos);
 }
 
+// Whether slice `slice` of `slices` left an item of several slices to join (at most bm rows, from row0 on of a sequence
+// that begins at first_row; `parts` partials, the first in `slot`), with every index that the join forms in
+// range: partials below 2 * slices, rows below total, heads below kv_heads * group.
+WHALE_HD inline bool cut_valid(const ChunkView& c, int group, int bm, int slices, int slice, int first_row, int row0,
+                               int n_rows, int head0, int parts, int slot) {
+  return parts > 1 && parts <= slices - slice && (slot >> 1) == slice && n_rows > 0 && n_rows <= bm && first_row >= 0 &&
+         row0 >= 0 && (long long)first_row + ((long long)row0 + n_rows - 1) / group < c.total && head0 >= 0 &&
+         head0 <= c.kv_heads * group - group;
+}
+
 // The scale's exponent of a row whose largest magnitude is amax (finite or infinite, no NaN).
 WHALE_HD inline int scale_exponent(float amax) {
   uint32_t u;
