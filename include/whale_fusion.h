@@ -464,7 +464,10 @@ whale_status whale_cache_read(const whale_config* cfg, const whale_cache* cache,
  * sequence's cached positions, q and a [total_new, n_heads * d_head] bf16 with row strides ld_q, ld_a. flags: 0, or
  * WHALE_ATTEND_CAUSAL: a row sees positions up to its own, lengths[b] - n_b + i. A row that sees nothing
  * (an empty history, a negative position) gives 0. Softmax statistics and sums are fp32; the weights that multiply V
- * are rounded to bf16, or on an e4m3 cache with up to 32 rows (max_new * n_heads / n_kv_heads) to f16. Results do not
+ * are rounded once: to bf16, or to f16 (11 bits, and within 2^-24 of the row's largest weight) for a sequence of
+ * few rows on an e4m3 cache. Rows are counted as n_b * n_heads / n_kv_heads, and few are up to 32 where max_new has no more either;
+ * in a batch with longer sequences up to 16 (or 32) where the batch has so many a sequence on average (total_new / B), else
+ * none. How V's scales differ from row to row does not matter to either. Results do not
  * depend on timing: repeated calls agree bit for bit. a must not overlap q. Supported: max_length <= 2^30,
  * total_new * n_heads < 2^31. Cached rows
  * within lengths[b] must be finite (a causal row's weights of later positions are 0, and 0 times an infinity

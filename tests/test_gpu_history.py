@@ -748,3 +748,51 @@ def test_serving_chain_matches_the_packed_path(fmt):
         if fmt == "bf16":
             got, other = _np(a[off[b]:off[b + 1]]).reshape(ref.shape), _np(packed[off[b]:off[b + 1]]).reshape(ref.shape)
             _close(got, other, 2 * _attend_tol(ref, mag), f"packed {b}")
+
+
+# ----------------------------------------------------------------------------------------------
+# values of very different sizes
+# ----------------------------------------------------------------------------------------------
+def _spread_values(rng, kind, length):
+    """Powers of two by which a history's V rows are multiplied."""
+    e = np.zeros(length)
+    if kind == "zero rows":        # whose scale stands for 1, beside rows of about 2^-30
+        e[:] = -30
+    elif kind == "tiny":           # the least scales
+        e[:] = -96
+    elif kind == "any":
+        e = rng.integers(-60, 61, length).astype(np.float64)
+    elif kind == "late":           # the last event, which only the last row may see, and one early one that all see
+        e[-1] = 40
+        e[length // 3] = 12
+    elif kind == "largest":        # the last event's numbers past the largest scale's
+        e[-1] = 127
+    return e
+
+
+@pytest.mark.parametrize("kind", ["zero rows", "tiny", "any", "late", "largest"])
+@pytest.mark.parametrize("n", [1, 5, 24, 40])
+@pytest.mark.parametrize("dh", [32, 64])
+def test_attention_over_e4m3_values_of_any_size(kind, n, dh):
+    """V rows of one history whose scales differ by up to 2^226: positions that a row does not see, and rows of
+    zeros, cost the others nothing. Up to 32 rows the weights are f16 of 2^(s - m) beside values of its own scale's
+    neighbourhood: off by half a step of 2^-24 / 2^-8 / 2^7 at most, 2^-24 of the largest weight, for each position."""
+    rng = np.random.default_rng(n + dh)
+    lengths = [40, 2000]
+    c = Cache(rng, lengths, [n, n], 4, 4, dh, 32, "e4m3", fill=False)
+    for b, length in enumerate(lengths):
+        v = c.values[b][:, 1] * (2.0 ** _spread_values(rng, kind, length))[:, None, None]
+        v = np.clip(v, -3.3e38, 3.3e38)
+        if kind == "zero rows":
+            v[rng.random(length) < 0.1] = 0.0
+        c.values[b][:, 1] = I.bf16_round(v.astype(np.float32)).astype(np.float64)
+    c.store([(b, 0, n_b) for b, n_b in enumerate(lengths)])
+    q = bf16_randn(rng, c.total, 4 * dh)
+    a = _attend(c, q, True)
+    for b, length in enumerate(lengths):
+        lo = int(c.off[b])
+        for i in range(n):
+            end = length - n + i + 1
+            ref, mag = H.attention(q[lo + i : lo + i + 1].reshape(1, 4, dh), c.values[b][:, 0], c.values[b][:, 1], True, end - 1)
+            small = 2.0 ** -24 * np.abs(c.values[b][:end, 1]).sum(0)[None]
+            _close(_np(a[lo + i : lo + i + 1]).reshape(ref.shape), ref, _attend_tol(ref, mag) + small, f"sequence {b} row {i}")

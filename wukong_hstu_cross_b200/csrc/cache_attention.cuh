@@ -22,8 +22,12 @@
 // row are contiguous (the order of d_head inside a product is free as long as q has the same), and the
 // positions of a tile are numbered so that a lane's scores are 8 neighbouring ones, whose scales it
 // reads as one word. K's scale multiplies the score, V's the weight. Queries are brought into f16's range by a
-// power of two of each row (exact down to 2^-39 of the row's largest), weights are 2^(s - m + 7 + e - E), E the largest V
-// exponent so far: 11 significant bits down to 2^-21 of the largest, where bf16 weights have 8.
+// power of two of each row (exact down to 2^-39 of the row's largest).
+// f16 weights have 11 significant bits, where bf16 ones have 8, but 2^-24 is their least step, so V's scales must not
+// push them there: a unit's positions are taken in passes, each with those whose scale is within 2^kCaWindow of the
+// largest one left, E (one pass where the scales are alike, as a history's are); a weight is 2^(s - m - 8 + 15 + e - E), off by
+// at most 2^-24 of the largest weight where it is less than 2^-13 of it. A pass's sums are fp32 of their own, times 2^(E - 15) added
+// to the row's: what a row does not see, and rows of zeros (whose e is 0), can shift nothing out of it.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -71,6 +75,7 @@ constexpr int ca_warps(bool fp8, int mt) { return fp8 && mt == 1 ? 12 : 8; }
 constexpr int kCaMinUnits = 2;  // a warp's least share where there is little work: 12.1 us for one row of 8 heads over
                                 // 5000 positions; with 4 the units take longer, with 1 the join does (12.9, 13.3 us)
 constexpr float kCaLazy = 8.0f; // log2 headroom before the reference is raised
+constexpr int kCaWindow = 8;    // log2 of the range of V's scales that one pass takes (e4m3)
 
 template <int DH, bool FP8, int MT>
 struct CaTile {
@@ -129,6 +134,15 @@ __device__ __forceinline__ void mma_f16_16816(float (&c)[4], uint32_t a0, uint32
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with zeros for the sums so far.
+__device__ __forceinline__ void mma_f16_16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                    uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
@@ -285,7 +299,6 @@ __global__ void __launch_bounds__(32 * ca_warps(FP8, MT), 1) cache_attend_kernel
     end_min = __reduce_min_sync(0xffffffffu, end_min);
 
     float o[MT][ND][4], mr[MT][2], l[MT][2];
-    int e_ref = 0;  // largest V scale code so far (e4m3)
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
 #pragma unroll
@@ -343,12 +356,18 @@ __global__ void __launch_bounds__(32 * ca_warps(FP8, MT), 1) cache_attend_kernel
     }
     int ahead = look(t_lo + STAGES - 1);
 
-    for (int i = t_lo; i < t_hi; ++i) {
-      cp_async_wait<STAGES - 2>();
-      __syncwarp();
-      fetch(i + STAGES - 1, ahead);
-      cp_async_commit();
-      ahead = look(i + STAGES);
+    bool more = false;  // e4m3: the unit has positions for another pass, those with V's code
+    int below = 256;    // below this
+    for (int i = t_lo; i < t_hi; i += !more) {
+      if (!more) {
+        cp_async_wait<STAGES - 2>();
+        __syncwarp();
+        fetch(i + STAGES - 1, ahead);
+        cp_async_commit();
+        ahead = look(i + STAGES);
+        below = 256;
+      }
+      const bool first = !more;
       const uint32_t st = ring + (uint32_t)((i - t_lo) % STAGES) * L::BYTES;
       const int pos = i * kCaTile;
 
@@ -398,27 +417,23 @@ __global__ void __launch_bounds__(32 * ca_warps(FP8, MT), 1) cache_attend_kernel
 
       // scales: K's into the scores, V's as factors of the weights (8 neighbouring positions a lane)
       uint64_t vf[NT];  // pairs
+      float o_unit = 0.f;  // e4m3: what 1 in the pass's sums is in o
       if constexpr (FP8) {
         const bool ok = pos + lane < s.len;  // rows past the end hold any code
         uint32_t ck, cv;
         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(ck) : "r"(st + 2 * L::PLANE + lane));
         asm volatile("ld.shared.u8 %0, [%1];" : "=r"(cv) : "r"(st + 2 * L::PLANE + kCaTile + lane));
-        cv = ok ? cv : 0u;
-        const int e_new = max(e_ref, (int)__reduce_max_sync(0xffffffffu, cv));
-        if (e_new != e_ref) {
-          const float f = e_ref == 0 ? 0.f : fast_exp2((float)(e_ref - e_new));
-          e_ref = e_new;
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[m][d][k] *= f;
-        }
-        // each lane makes its position's two factors, 2^e and 2^(e - E + 7); then a lane takes those of its 8 positions
+        cv = ok && (int)cv < below ? cv : 0u;
+        const int e_max = (int)__reduce_max_sync(0xffffffffu, cv);  // E + 127
+        const bool in = (int)cv + kCaWindow >= e_max;
+        more = __any_sync(0xffffffffu, cv != 0u && !in);
+        below = e_max - kCaWindow;
+        o_unit = __uint_as_float((uint32_t)max(e_max - 15, 0) << 23);
+        // each lane makes its position's two factors, 2^e and 2^(e - E + 15); then a lane takes those of its 8 positions
         const uint32_t fs = smem_u32(factors[warp]);
+        __syncwarp();
         asm volatile("st.shared.b32 [%0], %1;" ::"r"(fs + 4 * lane), "r"(ck << 23) : "memory");
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(fs + 128 + 4 * lane), "r"((uint32_t)max((int)cv - e_ref + 134, 0) << 23)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(fs + 128 + 4 * lane), "r"(in ? (cv - e_max + 142) << 23 : 0u)
                      : "memory");
         __syncwarp();
         uint64_t kf[NT];
@@ -494,7 +509,7 @@ __global__ void __launch_bounds__(32 * ca_warps(FP8, MT), 1) cache_attend_kernel
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const float ref = mr[m][hh] == -INFINITY ? 0.f : mr[m][hh];
+          const float ref = (mr[m][hh] == -INFINITY ? 0.f : mr[m][hh]) + (FP8 ? kCaLazy : 0.f);
           const uint64_t nr = f2pack(-ref, -ref);
           uint64_t sum2 = f2pack(0.f, 0.f);
 #pragma unroll
@@ -515,13 +530,13 @@ __global__ void __launch_bounds__(32 * ca_warps(FP8, MT), 1) cache_attend_kernel
           float sum, sum1;
           f2unpack(sum2, sum, sum1);
           sum += sum1;
-          l[m][hh] += sum;
+          l[m][hh] += first ? sum : 0.f;
         }
 
       // o += weights x V
+      if constexpr (!FP8) {
 #pragma unroll
-      for (int k = 0; k < NT / 2; ++k) {  // 16 positions a step: n-tiles 2 k and 2 k + 1 of the scores
-        if constexpr (!FP8) {
+        for (int k = 0; k < NT / 2; ++k)  // 16 positions a step: n-tiles 2 k and 2 k + 1 of the scores
 #pragma unroll
           for (int d = 0; d < ND; d += 2) {
             uint32_t b0, b1, b2, b3;
@@ -532,32 +547,53 @@ __global__ void __launch_bounds__(32 * ca_warps(FP8, MT), 1) cache_attend_kernel
               mma_bf16_16816(o[m][d + 1], pf[m][2 * k][0], pf[m][2 * k][1], pf[m][2 * k + 1][0], pf[m][2 * k + 1][1], b2, b3);
             }
           }
-        } else {
-          // column n of n-tile d is column n * ND + d of V: a lane's bytes are contiguous
-          uint32_t v[4][ND / 4];
+      } else {
+        // column n of n-tile d is column n * ND + d of V: a lane's bytes are contiguous
+        uint32_t v[NT / 2][4][ND / 4];
+#pragma unroll
+        for (int k = 0; k < NT / 2; ++k)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int r = 8 * t + 4 * k + x;
             if constexpr (DH == 64) {
               const uint2 w = lds64(st + vpl + L::at(r, g >> 1) + 8 * (g & 1));
-              v[x][0] = w.x;
-              v[x][1] = w.y;
+              v[k][x][0] = w.x;
+              v[k][x][1] = w.y;
             } else {
-              v[x][0] = lds32(st + vpl + L::at(r, g >> 2) + 4 * (g & 3));
+              v[k][x][0] = lds32(st + vpl + L::at(r, g >> 2) + 4 * (g & 3));
             }
           }
 #pragma unroll
-          for (int d = 0; d < ND; d += 2) {
+        for (int d = 0; d < ND; d += 2) {
+          float c[MT][2][4];
+#pragma unroll
+          for (int k = 0; k < NT / 2; ++k) {
             const uint32_t sel = (d & 2) ? 0x7362u : 0x5140u;  // bytes d, d + 1 of the two rows, interleaved
-            const uint32_t lo2 = __byte_perm(v[0][d / 4], v[1][d / 4], sel), hi2 = __byte_perm(v[2][d / 4], v[3][d / 4], sel);
+            const uint32_t lo2 = __byte_perm(v[k][0][d / 4], v[k][1][d / 4], sel);
+            const uint32_t hi2 = __byte_perm(v[k][2][d / 4], v[k][3][d / 4], sel);
             const uint32_t b0 = e4m3x2_f16x2((uint16_t)lo2), b1 = e4m3x2_f16x2((uint16_t)hi2);
             const uint32_t b2 = e4m3x2_f16x2((uint16_t)(lo2 >> 16)), b3 = e4m3x2_f16x2((uint16_t)(hi2 >> 16));
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-              mma_f16_16816(o[m][d], pf[m][2 * k][0], pf[m][2 * k][1], pf[m][2 * k + 1][0], pf[m][2 * k + 1][1], b0, b1);
-              mma_f16_16816(o[m][d + 1], pf[m][2 * k][0], pf[m][2 * k][1], pf[m][2 * k + 1][0], pf[m][2 * k + 1][1], b2, b3);
+              const uint32_t a0 = pf[m][2 * k][0], a1 = pf[m][2 * k][1], a2 = pf[m][2 * k + 1][0], a3 = pf[m][2 * k + 1][1];
+              if (k == 0) {
+                mma_f16_16816_first(c[m][0], a0, a1, a2, a3, b0, b1);
+                mma_f16_16816_first(c[m][1], a0, a1, a2, a3, b2, b3);
+              } else {
+                mma_f16_16816(c[m][0], a0, a1, a2, a3, b0, b1);
+                mma_f16_16816(c[m][1], a0, a1, a2, a3, b2, b3);
+              }
             }
           }
+          const uint64_t unit = f2pack(o_unit, o_unit);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int k = 0; k < 4; k += 2)
+                f2unpack(ffma2(f2pack(c[m][e][k], c[m][e][k + 1]), unit, f2pack(o[m][d + e][k], o[m][d + e][k + 1])),
+                         o[m][d + e][k], o[m][d + e][k + 1]);
         }
       }
     }
@@ -567,7 +603,6 @@ __global__ void __launch_bounds__(32 * ca_warps(FP8, MT), 1) cache_attend_kernel
     // the item's output where the slice holds all of it, else a partial
     const bool whole = t_lo == 0 && t_hi == s.units;
     const long long slot = 2 * gw + (u != u_lo);
-    const float unscale = FP8 ? __uint_as_float((uint32_t)max(e_ref - 7, 0) << 23) : 1.f;
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -577,7 +612,7 @@ __global__ void __launch_bounds__(32 * ca_warps(FP8, MT), 1) cache_attend_kernel
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         const int r = 16 * m + 8 * hh + g;
         if (r >= n_rows) continue;
-        const float f = whole ? (sum == 0.f ? 0.f : unscale / sum) : unscale;
+        const float f = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
         float* po = p.part_o + (slot * BM + r) * DH;
         const int tok = (r0 + r) / p.group, head = kvh * p.group + (r0 + r) % p.group;
         __nv_bfloat16* dst = p.a + (long long)(s.first_row + tok) * p.lda + head * DH;
