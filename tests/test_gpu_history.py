@@ -796,3 +796,26 @@ def test_attention_over_e4m3_values_of_any_size(kind, n, dh):
             ref, mag = H.attention(q[lo + i : lo + i + 1].reshape(1, 4, dh), c.values[b][:, 0], c.values[b][:, 1], True, end - 1)
             small = 2.0 ** -24 * np.abs(c.values[b][:end, 1]).sum(0)[None]
             _close(_np(a[lo + i : lo + i + 1]).reshape(ref.shape), ref, _attend_tol(ref, mag) + small, f"sequence {b} row {i}")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 24, 40])
+def test_attention_of_a_value_near_the_largest(fmt, n):
+    """V of 3e38 at one position, whose score exceeds all those before it by 2^5 (less than makes the running
+    reference rise): its weight times V stays finite."""
+    rng = np.random.default_rng(n)
+    c = Cache(rng, [2048], [n], 4, 4, 64, 64, fmt, fill=False)
+    k, v = np.zeros_like(c.values[0][:, 0]), np.zeros_like(c.values[0][:, 1])
+    k[:, :, 0] = -2.0
+    k[::8, :, 0] = 0.0
+    k[165, :, 0] = 3.5  # q 8: 28 / 8 / ln 2 = 5.05 in powers of two
+    v[165] = 3e38
+    v[165, :, ::3] = -2e38
+    c.values[0][:, 0], c.values[0][:, 1] = k, I.bf16_round(v.astype(np.float32)).astype(np.float64)
+    c.store([(0, 0, 2048)])
+    q = np.zeros((n, 256), np.float32)
+    q[:, ::64] = 8.0
+    a = _attend(c, q, False)
+    ref, mag = H.attention(q[:1].reshape(1, 4, 64), c.values[0][:, 0], c.values[0][:, 1], False, 0)
+    for i in range(n):
+        _close(_np(a[i : i + 1]).reshape(ref.shape), ref, _attend_tol(ref, mag), f"row {i}")

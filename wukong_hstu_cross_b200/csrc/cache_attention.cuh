@@ -74,7 +74,8 @@ constexpr int kCaTile = 32;     // positions of a unit
 constexpr int ca_warps(bool fp8, int mt) { return fp8 && mt == 1 ? 12 : 8; }
 constexpr int kCaMinUnits = 2;  // a warp's least share where there is little work: 12.1 us for one row of 8 heads over
                                 // 5000 positions; with 4 the units take longer, with 1 the join does (12.9, 13.3 us)
-constexpr float kCaLazy = 8.0f; // log2 headroom before the reference is raised
+constexpr float kCaLazy = 8.0f; // log2 headroom before the reference is raised; weights are 2^(s - reference - 8), at most
+                                // 1, so that one times the largest V is finite
 constexpr int kCaWindow = 8;    // log2 of the range of V's scales that one pass takes (e4m3)
 
 template <int DH, bool FP8, int MT>
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(32 * ca_warps(FP8, MT), 1) cache_attend_kernel
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const float ref = (mr[m][hh] == -INFINITY ? 0.f : mr[m][hh]) + (FP8 ? kCaLazy : 0.f);
+          const float ref = (mr[m][hh] == -INFINITY ? 0.f : mr[m][hh]) + kCaLazy;
           const uint64_t nr = f2pack(-ref, -ref);
           uint64_t sum2 = f2pack(0.f, 0.f);
 #pragma unroll

@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(cp_threads(FP8), 1) cache_attend_tc_kernel(con
           l *= f;
         }
         m_run = m_new;
-        const float ref = m_run == -INFINITY ? 0.f : m_run;
+        const float ref = (m_run == -INFINITY ? 0.f : m_run) + kCaLazy;
         const uint64_t sc2 = f2pack(p.scale_log2, p.scale_log2), nr2 = f2pack(-ref, -ref);
         {
           uint64_t ls[2] = {f2pack(0.f, 0.f), f2pack(0.f, 0.f)};
