@@ -819,3 +819,19 @@ def test_attention_of_a_value_near_the_largest(fmt, n):
     ref, mag = H.attention(q[:1].reshape(1, 4, 64), c.values[0][:, 0], c.values[0][:, 1], False, 0)
     for i in range(n):
         _close(_np(a[i : i + 1]).reshape(ref.shape), ref, _attend_tol(ref, mag), f"row {i}")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 20, 150])
+def test_a_bound_of_no_rows_is_reported(fmt, n):
+    """max_new 0 and sequences with rows: none is taken, all stay, and the call says so; lengths past max_length too."""
+    rng = np.random.default_rng(n)
+    c = Cache(rng, [300, 40], [n, 2], 4, 4, 32, 16, fmt)
+    q = _gpu(bf16_randn(rng, c.total, 128), "bf16")
+    for kw, code in ((dict(max_new=0), W.WHALE_DEVERR_OFFSETS), (dict(max_length=299), W.WHALE_DEVERR_PAGES),
+                     (dict(max_new=0, max_length=299), W.WHALE_DEVERR_OFFSETS | W.WHALE_DEVERR_PAGES)):
+        a, chunk = torch.full((c.total, 128), 7.0, device=DEV, dtype=torch.bfloat16), c.chunk(**kw)
+        W.whale_cache_attention(c.cfg, c.handle(), chunk, q, a, _ws(W.whale_cache_attention_workspace_size(c.cfg, c.handle(), chunk)))
+        torch.cuda.synchronize()
+        assert W.whale_get_device_error() == code
+        assert (a == 7.0).all() == ("max_new" in kw)

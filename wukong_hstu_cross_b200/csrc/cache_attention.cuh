@@ -115,6 +115,11 @@ __device__ __forceinline__ CaSeq ca_seq(const CacheAttnArgs& p, int b, int bm) {
   s.blocks = rows > p.rows_lo && rows <= p.rows_hi ? (rows + bm - 1) / bm : 0;
   return s;
 }
+// Rows beyond the host's bound of them, and positions beyond the cache's: by one block, whether or not the sequence has work.
+__device__ __forceinline__ void ca_report(const CacheAttnArgs& p, int b, const CaSeq& s) {
+  if (s.rows > s.take) atomicOr(&g_device_error, kErrOffsets);
+  if (s.rows > 0 && p.c.lengths[b] > s.len) atomicOr(&g_device_error, kErrPages);
+}
 __device__ __forceinline__ long long ca_units(const CacheAttnArgs& p, int b, int bm) {
   const CaSeq s = ca_seq(p, b, bm);
   return (long long)s.units * s.blocks * p.c.kv_heads;
@@ -182,7 +187,11 @@ __global__ void __launch_bounds__(32 * ca_warps(FP8, MT), 1) cache_attend_kernel
   const int run = (p.c.B + kCaThreads - 1) / kCaThreads;
   const int b_lo = min(p.c.B, tid * run), b_hi = min(p.c.B, b_lo + run);
   long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += ca_units(p, b, BM);
+  for (int b = b_lo; b < b_hi; ++b) {
+    const CaSeq s = ca_seq(p, b, BM);
+    mine += (long long)s.units * s.blocks * p.c.kv_heads;
+    if (blockIdx.x == 0) ca_report(p, b, s);
+  }
   long long scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -242,8 +251,6 @@ __global__ void __launch_bounds__(32 * ca_warps(FP8, MT), 1) cache_attend_kernel
     const int kvh = item / s.blocks, r0 = (item - kvh * s.blocks) * BM;
     const int n_rows = min(BM, s.take * p.group - r0);
     const long long pos0 = (long long)p.c.lengths[b] - s.rows;  // position of the sequence's first row
-    if (lane == 0 && p.c.lengths[b] > s.len) atomicOr(&g_device_error, kErrPages);
-    if (lane == 0 && s.rows > s.take) atomicOr(&g_device_error, kErrOffsets);
 
     // queries as A fragments, ends of the rows
     uint32_t qf[MT][KS][4];

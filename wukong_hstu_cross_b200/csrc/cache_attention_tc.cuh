@@ -269,7 +269,10 @@ __global__ void __launch_bounds__(cp_threads(FP8), 1) cache_attend_tc_kernel(con
     return cp_head_units(p, s, b, s.blocks) * p.c.kv_heads;
   };
   long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += seq_units(b);
+  for (int b = b_lo; b < b_hi; ++b) {
+    mine += seq_units(b);
+    if (blockIdx.x == 0) ca_report(p, b, ca_seq(p, b, kCpRows));
+  }
   long long scan = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -308,11 +311,9 @@ __global__ void __launch_bounds__(cp_threads(FP8), 1) cache_attend_tc_kernel(con
   if (lane == 0 && u_lo < u_hi) walk.begin(p, start_b, start_at, u_lo, u_hi - u_lo);
   __syncwarp();
 
-  // A segment's queries into its buffer, the producers' warps each a part of the rows, by cp.async; and its bounds' errors.
+  // A segment's queries into its buffer, the producers' warps each a part of the rows, by cp.async.
   auto queries = [&](int seg, int part) -> bool {
     constexpr int CH = L::ROW / 16, RPI = 32 / CH, PARTS = cp_producers(FP8);
-    if (part == 0 && lane == 0 && p.c.lengths[walk.b] > walk.s.len) atomicOr(&g_device_error, kErrPages);
-    if (part == 0 && lane == 0 && walk.s.rows > walk.s.take) atomicOr(&g_device_error, kErrOffsets);
     if (seg >= 2 && !warp_wait(&qfree[seg & 1], ((seg >> 1) - 1) & 1, abort_flag)) return false;
     const uint32_t q_base = smem_u32(smem + L::OFF_Q) + (seg & 1) * 2 * L::TILE;
 #pragma unroll 4
