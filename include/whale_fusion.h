@@ -472,7 +472,7 @@ whale_status whale_cache_read(const whale_config* cfg, const whale_cache* cache,
  * total_new * n_heads < 2^31. Cached rows
  * within lengths[b] must be finite (a causal row's weights of later positions are 0, and 0 times an infinity
  * is a NaN). Workspace: whale_cache_attention_workspace_size bytes, 256-byte aligned; nothing in it needs to be set or kept
- * between calls. */
+ * between calls, and one for larger bounds (max_new, total_new, B, max_length) serves smaller ones. */
 #define WHALE_ATTEND_CAUSAL 1u
 size_t whale_cache_attention_workspace_size(const whale_config* cfg, const whale_cache* cache,
                                             const whale_chunk* chunk);

@@ -281,3 +281,22 @@ def test_a_join_takes_only_cuts_in_range(tmp_path):
     forms no index outside them or the rows."""
     _run(tmp_path, "cuts.cpp", "g++", ["-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover",
                                        "-I", os.path.join(ROOT, "wukong_hstu_cross_b200", "csrc")], CUTS)
+
+
+@pytest.mark.parametrize("h,hk,dh", [(8, 8, 64), (8, 2, 64), (4, 1, 32), (16, 4, 32)])
+@pytest.mark.parametrize("fmt", [W.WHALE_CACHE_BF16, W.WHALE_CACHE_E4M3])
+def test_the_attention_workspace_of_larger_bounds_serves_smaller_ones(h, hk, dh, fmt):
+    """A program that allocates once, for its largest chunk: no smaller or sparser one may need more."""
+    cfg = _cfg(d=h * dh, h=h)
+    k = _cache(n_kv_heads=hk, format=fmt, scales=FAKE)
+    size = lambda n, total, B, length: W.whale_cache_attention_workspace_size(  # noqa: E731
+        cfg, k, _chunk(max_new=n, total_new=total, B=B, max_length=length, table_stride=1024))
+    news, totals, batches = (0, 1, 2, 4, 8, 9, 16, 17, 32, 33, 100, 4096), (1, 2, 16, 17, 33, 640, 2048, 1 << 18), (1, 2, 20, 64, 1500)
+    for lengths in (0, 100, 1 << 16):
+        for i, n in enumerate(news):
+            for j, total in enumerate(totals):
+                for b, B in enumerate(batches):
+                    got = size(n, total, B, lengths)
+                    assert got > 0
+                    for less in ((news[max(i - 1, 0)], total, B), (n, totals[max(j - 1, 0)], B), (n, total, batches[max(b - 1, 0)])):
+                        assert size(*less, lengths) <= got, ((n, total, B), less)

@@ -2752,7 +2752,7 @@ whale_status plan_cache_attention(const Shape& s, const whale_cache& k, const wh
   if (c.total_new * s.h >= (1ll << 31) || c.max_length > (1 << 30)) return WHALE_ERR_UNSUPPORTED;
   size_t slices = 0, rows_in_slots = 0;
   for (int bm : {16, 32, kCpRows}) {
-    if (bm != p->bm && bm != p->few) continue;
+    if (bm > p->bm) continue;  // every plan of smaller bounds too, so that one workspace serves them all
     const size_t n = (size_t)kNumSM * (bm == kCpRows ? 1 : ca_warps(k.format == WHALE_CACHE_E4M3, bm / 16));
     slices = std::max(slices, n);
     rows_in_slots = std::max(rows_in_slots, 2 * n * bm);
