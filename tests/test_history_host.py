@@ -300,3 +300,35 @@ def test_the_attention_workspace_of_larger_bounds_serves_smaller_ones(h, hk, dh,
                     assert got > 0
                     for less in ((news[max(i - 1, 0)], total, B), (n, totals[max(j - 1, 0)], B), (n, total, batches[max(b - 1, 0)])):
                         assert size(*less, lengths) <= got, ((n, total, B), less)
+
+
+def test_descriptors_of_another_device_are_refused(monkeypatch):
+    """Descriptors are checked when they are made and once more at the call, when another device may be current. Empty
+    calls, so that nothing is launched either way; CPU tensors stand for those of another device."""
+    import torch
+
+    zeros = lambda *s, dtype=torch.int32: torch.zeros(*s, dtype=dtype)  # noqa: E731
+    bf16 = torch.bfloat16
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    rows = W.head_rows(zeros(0, 256, dtype=bf16), zeros(32, dtype=torch.float32), zeros(0), y=zeros(0, 256, dtype=bf16))
+    grads = W.head_grads(zeros(0, 256, dtype=bf16), zeros(0, 256, dtype=bf16), zeros(32, dtype=torch.float32))
+    cache = W.make_cache(zeros(2, 2, 8, 16, 32, dtype=bf16))
+    chunk = W.make_chunk(zeros(1), zeros(0), zeros(0, 1), 0, 0, 0)
+    ws, cfg, rotary = zeros(1 << 16, dtype=torch.uint8), _cfg(), W.make_rotary(32)
+    calls = [
+        lambda: W.whale_norm_rotate(cfg, rotary, rows, None, stream=0),
+        lambda: W.whale_norm_rotate(cfg, rotary, None, rows, stream=0),
+        lambda: W.whale_norm_rotate_backward(cfg, rotary, None, None, grads, None, W.WHALE_BF16, FAKE, 0, stream=0),
+        lambda: W.whale_norm_rotate_backward(cfg, rotary, None, None, None, None, W.WHALE_BF16, ws, stream=0),
+        lambda: W.whale_cache_append(cfg, cache, _chunk(B=0), FAKE, stream=0),
+        lambda: W.whale_cache_read(cfg, _cache(), chunk, FAKE, stream=0),
+        lambda: W.whale_cache_attention(cfg, cache, _chunk(B=0), FAKE, FAKE, FAKE, 0, stream=0),
+        lambda: W.whale_cache_attention(cfg, _cache(), chunk, FAKE, FAKE, FAKE, 0, stream=0),
+        lambda: W.whale_cache_attention(cfg, _cache(), _chunk(B=0), FAKE, FAKE, ws, stream=0),
+    ]
+    for call in calls:
+        call()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for call in calls:
+        with pytest.raises(ValueError):
+            call()

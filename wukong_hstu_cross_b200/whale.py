@@ -420,6 +420,20 @@ def _rows_of(name, t, dtypes, ndim=2, device=None):
     return t
 
 
+def _same_device(device, *parts):
+    """Descriptors (and a workspace) are on the device that the call runs on: the current one when they were made
+    may have been another. Descriptors that were filled in by hand are not looked at."""
+    for p in parts:
+        d = p.get_device() if hasattr(p, "get_device") else getattr(p, "_device", None)
+        if d is None:
+            continue
+        if device is None:
+            import torch
+            device = torch.cuda.current_device()
+        if d != device:
+            raise ValueError(f"{type(p).__name__}: made on device {d}, called on {device}")
+
+
 def _ld(t) -> int:
     return int(t.stride(0)) if t.shape[0] > 1 and t.shape[1] > 0 else int(t.shape[1])
 
@@ -451,7 +465,7 @@ def head_rows(x, gain, positions, y=None) -> whale_head_rows:
             raise ValueError(f"y: {tuple(y.shape)} for x {tuple(x.shape)}")
     r = whale_head_rows(_ptr(x), _ptr(y), _ptr(gain), _ptr(positions), x.shape[0], _ld(x), 0 if y is None else _ld(y),
                         x.shape[1] // gain.numel())
-    r._keepalive = (x, gain, positions, y)
+    r._keepalive, r._device = (x, gain, positions, y), x.get_device()
     return r
 
 
@@ -464,7 +478,7 @@ def head_grads(dy, dx, d_gain) -> whale_head_grads:
     if dx.shape != dy.shape:
         raise ValueError(f"dx: {tuple(dx.shape)} for dy {tuple(dy.shape)}")
     r = whale_head_grads(_ptr(dy), _ptr(dx), _ptr(d_gain), _ld(dy), _ld(dx))
-    r._keepalive = (dy, dx, d_gain)
+    r._keepalive, r._device = (dy, dx, d_gain), dy.get_device()
     return r
 
 
@@ -493,6 +507,7 @@ def _ref(s):
 def whale_norm_rotate(cfg, rotary, q, k, stream=None, raw=False):
     """Per-head RMS norm and rotation by position (see include/whale_fusion.h); q, k: head_rows or None."""
     _types(cfg, (q, k))
+    _same_device(None, q, k)
     st = _lib.whale_norm_rotate(ctypes.byref(cfg), ctypes.byref(rotary), _ref(q), _ref(k), _stream(stream))
     if raw:
         return st
@@ -506,6 +521,7 @@ def whale_norm_rotate_workspace_size(cfg, q, k) -> int:
 def whale_norm_rotate_backward(cfg, rotary, q, k, dq, dk, grad_dtype, workspace, workspace_bytes=None, stream=None,
                                raw=False):
     _types(cfg, (q, k), (dq, dk), grad_dtype)
+    _same_device(None, q, k, dq, dk, workspace)
     st = _lib.whale_norm_rotate_backward(ctypes.byref(cfg), ctypes.byref(rotary), _ref(q), _ref(k), _ref(dq), _ref(dk),
                                          int(grad_dtype), _ptr(workspace), _ws_bytes(workspace, workspace_bytes),
                                          _stream(stream))
@@ -528,7 +544,7 @@ def make_cache(pages, scales=None) -> whale_cache:
         raise ValueError("pages and scales must be contiguous")
     k = whale_cache(_ptr(pages), _ptr(scales), pages.shape[0], pages.shape[3], pages.shape[2],
                     WHALE_CACHE_E4M3 if e4m3 else WHALE_CACHE_BF16)
-    k._keepalive = (pages, scales)
+    k._keepalive, k._device = (pages, scales), pages.get_device()
     return k
 
 
@@ -545,7 +561,7 @@ def make_chunk(offsets, lengths, page_table, max_new, max_length, total_new) -> 
         raise ValueError("page_table must be contiguous")
     c = whale_chunk(_ptr(offsets), _ptr(lengths), _ptr(page_table), page_table.shape[1], lengths.numel(), int(max_new),
                     int(max_length), int(total_new))
-    c._keepalive = (offsets, lengths, page_table)
+    c._keepalive, c._device = (offsets, lengths, page_table), offsets.get_device()
     return c
 
 
@@ -588,6 +604,7 @@ def whale_cache_scales_size(cfg, cache) -> int:
 def whale_cache_append(cfg, cache, chunk, kv, stream=None, raw=False):
     """Write the chunk's K|V rows to the cache, in its format."""
     handle, device = _stream_on(stream)
+    _same_device(device, cache, chunk)
     ld = _packed("kv", kv, cfg, cache, chunk, _kv_width(cfg, cache), device)
     st = _lib.whale_cache_append(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk), _ptr(kv), ld, handle)
     if raw:
@@ -598,6 +615,7 @@ def whale_cache_append(cfg, cache, chunk, kv, stream=None, raw=False):
 def whale_cache_read(cfg, cache, chunk, kv, stream=None, raw=False):
     """Read the chunk's K|V rows back from the cache, as bf16."""
     handle, device = _stream_on(stream)
+    _same_device(device, cache, chunk)
     ld = _packed("kv", kv, cfg, cache, chunk, _kv_width(cfg, cache), device)
     st = _lib.whale_cache_read(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk), _ptr(kv), ld, handle)
     if raw:
@@ -612,6 +630,7 @@ def whale_cache_attention_workspace_size(cfg, cache, chunk) -> int:
 def whale_cache_attention(cfg, cache, chunk, q, a, workspace, workspace_bytes=None, flags=0, stream=None, raw=False):
     """Attention of the chunk's rows q over the cached histories (flags: WHALE_ATTEND_CAUSAL) into a."""
     handle, device = _stream_on(stream)
+    _same_device(device, cache, chunk, workspace)
     ldq, lda = _packed("q", q, cfg, cache, chunk, cfg.d, device), _packed("a", a, cfg, cache, chunk, cfg.d, device)
     st = _lib.whale_cache_attention(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk), _ptr(q), ldq, _ptr(a),
                                     lda, int(flags), _ptr(workspace), _ws_bytes(workspace, workspace_bytes), handle)
