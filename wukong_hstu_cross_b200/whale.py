@@ -60,20 +60,24 @@ class whale_rotary(ctypes.Structure):
 
 
 class whale_head_rows(ctypes.Structure):
+    _device = None  # of the tensors, where the binding made it
     _fields_ = [("x", c_void_p), ("y", c_void_p), ("gain", c_void_p), ("positions", c_void_p), ("rows", c_longlong),
                 ("ld_x", c_longlong), ("ld_y", c_longlong), ("n_heads", c_int)]
 
 
 class whale_head_grads(ctypes.Structure):
+    _device = None  # of the tensors, where the binding made it
     _fields_ = [("dy", c_void_p), ("dx", c_void_p), ("d_gain", c_void_p), ("ld_dy", c_longlong), ("ld_dx", c_longlong)]
 
 
 class whale_cache(ctypes.Structure):
+    _device = None  # of the tensors, where the binding made it
     _fields_ = [("pages", c_void_p), ("scales", c_void_p), ("n_pages", c_int), ("page_size", c_int),
                 ("n_kv_heads", c_int), ("format", c_int)]
 
 
 class whale_chunk(ctypes.Structure):
+    _device = None  # of the tensors, where the binding made it
     _fields_ = [("offsets", c_void_p), ("lengths", c_void_p), ("page_table", c_void_p), ("table_stride", c_int),
                 ("B", c_int), ("max_new", c_int), ("max_length", c_int), ("total_new", c_longlong)]
 
@@ -420,18 +424,32 @@ def _rows_of(name, t, dtypes, ndim=2, device=None):
     return t
 
 
-def _same_device(device, *parts):
-    """Descriptors (and a workspace) are on the device that the call runs on: the current one when they were made
-    may have been another. Descriptors that were filled in by hand are not looked at."""
+def _stream_on(stream):
+    """(stream handle, device of the call; None: the current one, not looked up)."""
+    if stream is None:
+        import torch
+        device = torch.cuda.current_device()  # given to current_stream, it halves the look-up (1.5 us for 3.2)
+        return torch.cuda.current_stream(device).cuda_stream, device
+    return _stream(stream), None
+
+
+def _same_device(device, workspace, *parts):
+    """Descriptors and workspace are on the device that the call runs on (None: the current one); when a descriptor was
+    made another may have been current. Those that were filled in by hand are not looked at."""
     for p in parts:
-        d = p.get_device() if hasattr(p, "get_device") else getattr(p, "_device", None)
-        if d is None:
-            continue
-        if device is None:
-            import torch
-            device = torch.cuda.current_device()
-        if d != device:
-            raise ValueError(f"{type(p).__name__}: made on device {d}, called on {device}")
+        if p is not None and p._device != device and p._device is not None:
+            device = _on(p._device, device)
+    if workspace is not None and not isinstance(workspace, int) and workspace.get_device() != device:
+        _on(workspace.get_device(), device)
+
+
+def _on(made, device):
+    if device is None:
+        import torch
+        device = torch.cuda.current_device()
+    if made != device:
+        raise ValueError(f"tensors on device {made}, a call on device {device}")
+    return device
 
 
 def _ld(t) -> int:
@@ -506,9 +524,10 @@ def _ref(s):
 
 def whale_norm_rotate(cfg, rotary, q, k, stream=None, raw=False):
     """Per-head RMS norm and rotation by position (see include/whale_fusion.h); q, k: head_rows or None."""
+    handle, device = _stream_on(stream)
     _types(cfg, (q, k))
-    _same_device(None, q, k)
-    st = _lib.whale_norm_rotate(ctypes.byref(cfg), ctypes.byref(rotary), _ref(q), _ref(k), _stream(stream))
+    _same_device(device, None, q, k)
+    st = _lib.whale_norm_rotate(ctypes.byref(cfg), ctypes.byref(rotary), _ref(q), _ref(k), handle)
     if raw:
         return st
     _check(st, "whale_norm_rotate")
@@ -520,11 +539,11 @@ def whale_norm_rotate_workspace_size(cfg, q, k) -> int:
 
 def whale_norm_rotate_backward(cfg, rotary, q, k, dq, dk, grad_dtype, workspace, workspace_bytes=None, stream=None,
                                raw=False):
+    handle, device = _stream_on(stream)
     _types(cfg, (q, k), (dq, dk), grad_dtype)
-    _same_device(None, q, k, dq, dk, workspace)
+    _same_device(device, workspace, q, k, dq, dk)
     st = _lib.whale_norm_rotate_backward(ctypes.byref(cfg), ctypes.byref(rotary), _ref(q), _ref(k), _ref(dq), _ref(dk),
-                                         int(grad_dtype), _ptr(workspace), _ws_bytes(workspace, workspace_bytes),
-                                         _stream(stream))
+                                         int(grad_dtype), _ptr(workspace), _ws_bytes(workspace, workspace_bytes), handle)
     if raw:
         return st
     _check(st, "whale_norm_rotate_backward")
@@ -565,15 +584,6 @@ def make_chunk(offsets, lengths, page_table, max_new, max_length, total_new) -> 
     return c
 
 
-def _stream_on(stream):
-    """(stream handle, current device): one look at the current stream gives both."""
-    import torch
-    if stream is None:
-        st = torch.cuda.current_stream()
-        return st.cuda_stream, st.device_index
-    return _stream(stream), None
-
-
 def _packed(name, t, cfg, cache, chunk, width, device):
     """A packed [total_new, width] bf16 tensor's row stride, and the cache's planes and d_head, checked."""
     import torch
@@ -604,7 +614,7 @@ def whale_cache_scales_size(cfg, cache) -> int:
 def whale_cache_append(cfg, cache, chunk, kv, stream=None, raw=False):
     """Write the chunk's K|V rows to the cache, in its format."""
     handle, device = _stream_on(stream)
-    _same_device(device, cache, chunk)
+    _same_device(device, None, cache, chunk)
     ld = _packed("kv", kv, cfg, cache, chunk, _kv_width(cfg, cache), device)
     st = _lib.whale_cache_append(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk), _ptr(kv), ld, handle)
     if raw:
@@ -615,7 +625,7 @@ def whale_cache_append(cfg, cache, chunk, kv, stream=None, raw=False):
 def whale_cache_read(cfg, cache, chunk, kv, stream=None, raw=False):
     """Read the chunk's K|V rows back from the cache, as bf16."""
     handle, device = _stream_on(stream)
-    _same_device(device, cache, chunk)
+    _same_device(device, None, cache, chunk)
     ld = _packed("kv", kv, cfg, cache, chunk, _kv_width(cfg, cache), device)
     st = _lib.whale_cache_read(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk), _ptr(kv), ld, handle)
     if raw:
@@ -630,7 +640,7 @@ def whale_cache_attention_workspace_size(cfg, cache, chunk) -> int:
 def whale_cache_attention(cfg, cache, chunk, q, a, workspace, workspace_bytes=None, flags=0, stream=None, raw=False):
     """Attention of the chunk's rows q over the cached histories (flags: WHALE_ATTEND_CAUSAL) into a."""
     handle, device = _stream_on(stream)
-    _same_device(device, cache, chunk, workspace)
+    _same_device(device, workspace, cache, chunk)
     ldq, lda = _packed("q", q, cfg, cache, chunk, cfg.d, device), _packed("a", a, cfg, cache, chunk, cfg.d, device)
     st = _lib.whale_cache_attention(ctypes.byref(cfg), ctypes.byref(cache), ctypes.byref(chunk), _ptr(q), ldq, _ptr(a),
                                     lda, int(flags), _ptr(workspace), _ws_bytes(workspace, workspace_bytes), handle)
