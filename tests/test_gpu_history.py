@@ -835,3 +835,40 @@ def test_a_bound_of_no_rows_is_reported(fmt, n):
         torch.cuda.synchronize()
         assert W.whale_get_device_error() == code
         assert (a == 7.0).all() == ("max_new" in kw)
+
+
+@pytest.mark.parametrize("shared", [False, True])
+def test_a_layer_whose_histories_are_cached(shared):
+    """A whole fusion layer with its history cached in two appends: project, append, query projection, attention over the cache,
+    fusion MLP and FFN, against the oracle of the layer and the layer's own entry point, both at the bound of whole layers."""
+    from tests.gpu_util import BF16_TOL, assert_parity
+    from oracle import whale_oracle as O
+    from wukong_hstu_cross_b200 import harness as Hn
+    w = I.WORKLOADS["stack_d256"].replace(batch=3, n_layers=1, lengths=("uniform", 1, 900))
+    p = Hn.build_problem(w, gains="random", shared_kv=shared)
+    lw, N, d, h, B = p.weights[0], w.n_tokens, w.d, w.n_heads, w.batch
+    c = Cache(np.random.default_rng(0), p.lengths, p.lengths, h, h, d // h, 64, "bf16", shared, fill=False)
+    ws = _ws(64 << 20)
+    lo = np.zeros(B, np.int64)
+    for hi in (p.lengths // 2, p.lengths):
+        rows = torch.cat([p.states[0, p.offsets[b] + lo[b] : p.offsets[b] + hi[b]] for b in range(B)])
+        kv = torch.empty(rows.shape[0], c.width(), device=DEV, dtype=torch.bfloat16)
+        W.whale_project_kv(p.cfg, rows.shape[0], rows, lw["g_kv"], lw["w_kv"], kv, ws)
+        new = hi - lo
+        W.whale_cache_append(p.cfg, c.handle(), c.chunk(offsets=_int(np.concatenate([[0], np.cumsum(new)])), lengths=_int(hi),
+                                                        max_new=int(new.max()), total_new=int(new.sum())), kv)
+        lo = hi
+    x = p.tokens.reshape(B * N, d)
+    q, a, f, y = (torch.empty_like(x) for _ in range(4))
+    W.whale_project_queries(p.cfg, B * N, x, lw["g_q"], lw["w_q"], q, ws)
+    chunk = c.chunk(offsets=_int(np.arange(B + 1) * N), max_new=N, total_new=B * N)
+    W.whale_cache_attention(p.cfg, c.handle(), chunk, q, a, ws)
+    W.whale_fusion_mlp(p.cfg, B * N, a, x, lw["w_f1"], lw["w_f2"], f, ws)
+    W.whale_swiglu_ffn(p.cfg, B * N, f, lw["g_ffn"], lw["w_upgate"], lw["w_down"], y, ws)
+    layer = Hn.run_forward(p)
+    torch.cuda.synchronize()
+    for b in range(B):
+        ref = O.fusion_stack_example(I.tokens_of_example(w, b), Hn.states_of_example_host(p, b), p.host_weights, h, w.eps, **p.flags)
+        got = y.reshape(B, N, d)[b]
+        assert_parity(got, ref, "bf16", rms_rel=2e-2, what=f"example {b}")
+        assert np.all(np.abs(_np(got) - _np(layer[b])) <= 2 * BF16_TOL * (1.0 + np.abs(ref)))
