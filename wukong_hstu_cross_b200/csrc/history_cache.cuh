@@ -39,12 +39,14 @@ struct RowsArgs {
   const __nv_bfloat16* src;  // append: kv [total, ld]
   __nv_bfloat16* dst;        // read: kv [total, ld]
   long long ld;
-  int rows_per_block;  // read: <= kRowsThreads
   uint8_t* pages;
   uint8_t* scales;
 };
 
 constexpr int kRowsThreads = 256;
+// Rows of a block: one pass of its threads, 16 bytes of a head each (two passes of the read took 65 us where one takes 61:
+// 48 histories, d 256, e4m3).
+constexpr int rows_per_block(int dh) { return kRowsThreads / (dh / 8); }
 // Heads whose 16 bytes a lane has in flight at once (append: and as many more while it uses those).
 constexpr int kAppendHeads = 4, kReadHeads = 8;
 
@@ -118,14 +120,14 @@ __global__ void __launch_bounds__(kRowsThreads, 5) cache_append_kernel(const Row
 // histories of 3000 to 6000 rows, d 256, e4m3).
 template <int DH, bool FP8>
 __global__ void __launch_bounds__(kRowsThreads) cache_read_kernel(const RowsArgs a) {
-  constexpr int LPH = DH / 8, HU = kReadHeads, ROWS = kRowsThreads / LPH;
-  __shared__ long long places[kRowsThreads];
+  constexpr int LPH = DH / 8, HU = kReadHeads, ROWS = rows_per_block(DH);
+  __shared__ long long places[ROWS];
   pdl_wait();
   pdl_trigger();
   const int li = threadIdx.x % LPH;
-  const long long first = (long long)blockIdx.x * a.rows_per_block;
+  const long long first = (long long)blockIdx.x * ROWS;
   const int heads = a.c.planes * a.c.kv_heads;
-  if ((int)threadIdx.x < a.rows_per_block) {
+  if (threadIdx.x < ROWS) {
     const long long row = first + threadIdx.x;
     long long at = -2;  // behind the last sequence; -1: in no page
     if (row < a.c.total && row < a.c.offsets[a.c.B]) {
@@ -136,45 +138,48 @@ __global__ void __launch_bounds__(kRowsThreads) cache_read_kernel(const RowsArgs
     places[threadIdx.x] = at;
   }
   __syncthreads();
-  for (int r = threadIdx.x / LPH; r < a.rows_per_block; r += ROWS) {
-    const long long at = places[r];
-    if (at == -2) break;
-    uint4* dst = reinterpret_cast<uint4*>(a.dst + (first + r) * a.ld) + li;
-    for (int h0 = 0; h0 < heads; h0 += HU) {
-      uint4 w[HU];
-      uint32_t sc[HU];
+  const int r = threadIdx.x / LPH;
+  const long long at = places[r];
+  if (at == -2) return;
+  uint4* dst = reinterpret_cast<uint4*>(a.dst + (first + r) * a.ld) + li;
+  for (int h0 = 0; h0 < heads; h0 += HU) {
+    uint4 w[HU];
+    uint32_t sc[HU];
 #pragma unroll
-      for (int k = 0; k < HU; ++k) {
-        w[k] = make_uint4(0u, 0u, 0u, 0u);
-        sc[k] = 0u;
-        if (at >= 0 && h0 + k < heads) {
-          const long long in = at + ((long long)(h0 + k) << a.c.page_shift);
-          if constexpr (!FP8) {
-            w[k] = *reinterpret_cast<const uint4*>(a.pages + (in * DH + li * 8) * 2);
-          } else {
-            const uint2 q = *reinterpret_cast<const uint2*>(a.pages + in * DH + li * 8);
-            w[k].x = q.x;
-            w[k].y = q.y;
-            sc[k] = a.scales[in];
-          }
+    for (int k = 0; k < HU; ++k) {
+      w[k] = make_uint4(0u, 0u, 0u, 0u);
+      sc[k] = 0u;
+      if (at >= 0 && h0 + k < heads) {
+        const long long in = at + ((long long)(h0 + k) << a.c.page_shift);
+        if constexpr (!FP8) {
+          w[k] = *reinterpret_cast<const uint4*>(a.pages + (in * DH + li * 8) * 2);
+        } else {
+          const uint2 q = *reinterpret_cast<const uint2*>(a.pages + in * DH + li * 8);
+          w[k].x = q.x;
+          w[k].y = q.y;
         }
       }
+    }
+    if constexpr (FP8) {  // behind all numbers: 60.6 us; each scale beside its head's numbers 69 us (the same histories)
 #pragma unroll
-      for (int k = 0; k < HU; ++k) {
-        if (h0 + k >= heads) break;
-        if constexpr (FP8) {
-          const float f = __uint_as_float(sc[k] << 23);
-          uint32_t o[4];
+      for (int k = 0; k < HU; ++k)
+        if (at >= 0 && h0 + k < heads) sc[k] = a.scales[at + ((long long)(h0 + k) << a.c.page_shift)];
+    }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t v = e4m3x2_f16x2((uint16_t)((i < 2 ? w[k].x : w[k].y) >> (16 * (i & 1))));
-            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v));
-            o[i] = pack_bf16x2(x.x * f, x.y * f);
-          }
-          w[k] = make_uint4(o[0], o[1], o[2], o[3]);
+    for (int k = 0; k < HU; ++k) {
+      if (h0 + k >= heads) break;
+      if constexpr (FP8) {
+        const float f = __uint_as_float(sc[k] << 23);
+        uint32_t o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t v = e4m3x2_f16x2((uint16_t)((i < 2 ? w[k].x : w[k].y) >> (16 * (i & 1))));
+          const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&v));
+          o[i] = pack_bf16x2(x.x * f, x.y * f);
         }
-        dst[(h0 + k) * LPH] = w[k];
+        w[k] = make_uint4(o[0], o[1], o[2], o[3]);
       }
+      dst[(h0 + k) * LPH] = w[k];
     }
   }
 }
