@@ -872,3 +872,19 @@ def test_a_layer_whose_histories_are_cached(shared):
         got = y.reshape(B, N, d)[b]
         assert_parity(got, ref, "bf16", rms_rel=2e-2, what=f"example {b}")
         assert np.all(np.abs(_np(got) - _np(layer[b])) <= 2 * BF16_TOL * (1.0 + np.abs(ref)))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 24, 40])
+def test_attention_of_queries_near_the_largest(fmt, n):
+    """Queries with one number of 2^122 and more where the keys are zero, the others 2^-19 of it and exact in f16 beside it:
+    finite scores of about 1."""
+    rng = np.random.default_rng(n)
+    c = Cache(rng, [300], [n], 4, 4, 64, 64, fmt, fill=False)
+    c.values[0][:, 0] *= 2.0 ** -103
+    c.values[0][:, 0, :, 0] = 0.0
+    c.store([(0, 0, 300)])
+    q = bf16_randn(rng, n, 256, scale=2.0 ** 103)
+    q[:, ::64] = 2.0 ** rng.integers(121, 124, (n, 4))
+    a = _attend(c, q, False)
+    _check_attend(c, q, a, False)

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(32 * ca_warps(FP8, MT), 1) cache_attend_kernel
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           int ex = (int)(__float_as_uint(mx) >> 23) - 127;  // mx in [2^ex, 2^(ex+1))
-          ex = mx == 0.f ? 14 : max(-100, min(ex, 120));
+          ex = mx == 0.f ? 14 : max(-100, min(ex, 127));
           const float down = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
           fac[m][hh] = p.scale_log2 * __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
 #pragma unroll
