@@ -888,3 +888,31 @@ def test_attention_of_queries_near_the_largest(fmt, n):
     q[:, ::64] = 2.0 ** rng.integers(121, 124, (n, 4))
     a = _attend(c, q, False)
     _check_attend(c, q, a, False)
+
+
+@pytest.mark.parametrize("fmt,dh", [("bf16", 64), ("e4m3", 32)])
+def test_a_pool_past_32_bits(fmt, dh):
+    """The same pages in a small pool and at the end of one of 4.5 GB: equal results of every operator."""
+    rng = np.random.default_rng(dh)
+    for n in (1, 20, 150):
+        c = Cache(rng, [700, 200], [n, n], 8, 8, dh, 64, fmt)
+        q, kv = _gpu(bf16_randn(rng, c.total, 8 * dh), "bf16"), _gpu(bf16_randn(rng, c.total, c.width()), "bf16")
+        pool = (9 << 29) // c.pages[0].nbytes
+        big = torch.empty(pool, *c.pages.shape[1:], device=DEV, dtype=c.pages.dtype)
+        scales = None if c.scales is None else torch.empty(pool, *c.scales.shape[1:], device=DEV, dtype=torch.uint8)
+        big[-c.n_pages:].copy_(c.pages)
+        if scales is not None:
+            scales[-c.n_pages:].copy_(c.scales)
+        out = []
+        for cache, table in ((c.handle(), c.table), (W.make_cache(big, scales), np.where(c.table < 0, -1, c.table + pool - c.n_pages))):
+            chunk = c.chunk(page_table=_int(table))
+            a, back = torch.empty_like(q), torch.empty_like(kv)
+            W.whale_cache_attention(c.cfg, cache, chunk, q, a, _ws(W.whale_cache_attention_workspace_size(c.cfg, cache, chunk)))
+            W.whale_cache_append(c.cfg, cache, chunk, kv)
+            W.whale_cache_read(c.cfg, cache, chunk, back)
+            out.append((a, back))
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(*out))
+        assert torch.equal(big[-c.n_pages:].view(torch.uint8), c.pages.view(torch.uint8))
+        if scales is not None:
+            assert torch.equal(scales[-c.n_pages:], c.scales)
