@@ -350,14 +350,16 @@ whale_status whale_fusion_backward(const whale_config* cfg, const void* wukong_t
  *   t = position * base^(-2 i / rotary_dim);  the other columns stay n.
  * Rotated queries and keys have scores that depend on the difference of their positions. No counterpart in the
  * pages: their attention has no positional term; a history that is cached row by row needs one that is
- * applied to each row once. eps is cfg->eps; cfg->n_heads and the sizes of the other steps are not
- * read, d_head = d / n_heads. */
+ * applied to each row once. Of cfg, the type, eps and d_head = d / n_heads count here (how many heads the rows have
+ * is said with them); the other fields are checked as everywhere. With WHALE_SHARED_KV the K rows are the V rows too:
+ * rotated in place, before whale_cache_append, they are rotated as values as well; a model whose values are
+ * not rotated keeps K and V apart. */
 enum { WHALE_ROTATE_HALVES = 0,   /* pair i = columns i and i + rotary_dim / 2 */
        WHALE_ROTATE_ADJACENT = 1  /* pair i = columns 2 i and 2 i + 1 */ };
 typedef struct {
   int rotary_dim; /* 0 (no rotation) .. d_head, a multiple of 16 (bf16) or 8 (fp32) */
   int layout;     /* WHALE_ROTATE_* */
-  double base;    /* > 0; 10000 is usual */
+  double base;    /* > 0; 10000 is usual, below 1 the angles grow with i and lose what whale_norm_rotate says of them */
 } whale_rotary;
 
 /* The queries, or the keys, of one call. Rows of x and y are n_heads * d_head numbers of cfg->dtype, ld_*
@@ -374,13 +376,15 @@ typedef struct {
 } whale_head_rows;
 
 /* q, k: host structs (device pointers inside); either may be null. One kernel for both. Sums are kept in fp32 and
- * rounded once, to cfg->dtype; angles are reduced in 64-bit fixed point, exact to 2^-32 of a turn at any position;
+ * rounded once, to cfg->dtype; angles are reduced in 64-bit fixed point, within 2^-31 of a turn at any position (base >= 1;
+ * 2^-20 for a base of 0.001);
  * sines and cosines are off by 2^-20 at most in bf16 mode, and as accurate as fp32 holds them in fp32 mode.
  * d_head: 32 or 64 in bf16 mode; 8, 16, 32, 64 or 128 in fp32 mode. */
 whale_status whale_norm_rotate(const whale_config* cfg, const whale_rotary* rotary, const whale_head_rows* q,
                                const whale_head_rows* k, whale_stream_t stream);
 
-/* Its backward pass: from x (the forward's input) and dy = dLoss/dy, with dn = the pairs of dy turned back,
+/* Its backward pass, for training loops with an attention backward of their own: whale_fusion_backward and
+ * whale_fusion_layer_backward are whole layers, whose queries and keys are neither normalised per head nor rotated. From x (the forward's input) and dy = dLoss/dy, with dn = the pairs of dy turned back,
  *   d_gain = sum over rows and heads of dn * x * r,   r = 1 / sqrt(mean(x^2) + eps)
  *   dx     = r * dn * gain - x * r^3 * mean(dn * gain * x)
  * dy and dx have type grad_dtype (WHALE_FP32, or WHALE_BF16 in bf16 mode); d_gain is fp32. dx and d_gain are
@@ -414,7 +418,7 @@ whale_status whale_norm_rotate_backward(const whale_config* cfg, const whale_rot
  * WHALE_CACHE_BF16 keeps the projected rows as they are. WHALE_CACHE_E4M3 keeps e4m3 numbers
  * that stand for number * 2^e, e = scale - 127 the least integer in [-100, 119] with max|row| <= 448 * 2^e (0 for a
  * row of zeros): the scaling is exact, each number is rounded once (to nearest even), and reads are exact in bf16. NaNs
- * stay NaNs and do not count for e; infinities become +-448 * 2^119. */
+ * stay NaNs and do not count for e; infinities, and numbers beyond it, become +-448 * 2^119. */
 typedef enum { WHALE_CACHE_BF16 = 0, WHALE_CACHE_E4M3 = 1 } whale_cache_format;
 typedef struct {
   void* pages;            /* device, 16-byte aligned, whale_cache_pages_size bytes */

@@ -6,7 +6,7 @@
 // sequence and K|V head share every cached row: row r is token r / group, head kvh * group + r % group.
 //
 // Bound: HBM (each cached row is read once; 2 * n_b * group operations per byte of bf16).
-// 64 users, d 512, histories of up to 15000 rows: one row 139 us (bf16, 6.2 TB/s) and 101 us (e4m3), 32 rows 160 and 165 us.
+// 64 users, d 512, histories of up to 15000 rows: one row 138 to 144 us (bf16, 6.0 to 6.2 TB/s) and 100 us (e4m3), 32 rows 159 and 171 us.
 //
 // Split. Units of kCaTile positions of one (sequence, K|V head, block of BM rows) are laid end to end, and warp w of
 // W takes the contiguous slice [w T / W, (w + 1) T / W): every warp streams the same number of bytes whatever the
@@ -17,17 +17,19 @@
 // The stream: cp.async, STAGES - 1 tiles ahead; the lanes look up the page of one position each, a tile earlier still.
 // Rows past the end and rows in no page are zero-filled, so what unwritten rows hold is never used.
 //
-// Products: warp-level m16n8k16 with fp32 sums. bf16 cache: K and V by ldmatrix. e4m3 cache: the
-// fragments are converted from the bytes in registers, to f16 (every e4m3 number is an f16 number); a lane's bytes of a K
-// row are contiguous (the order of d_head inside a product is free as long as q has the same), and the
+// Products: warp-level m16n8k16 with fp32 sums. bf16 cache: K and V by ldmatrix; weights are rounded to bf16, V's
+// type, which both operands of a product have (one event's relative error is then 0.0023 where the rounding of the result
+// alone leaves 0.0016; the packed path rounds its weights the same way). e4m3 cache: the fragments are converted from the bytes in registers, to f16 (every e4m3 number is an f16 number); a lane's bytes of a K row are contiguous (the order of d_head inside a product is free as long as q has the same), and the
 // positions of a tile are numbered so that a lane's scores are 8 neighbouring ones, whose scales it
 // reads as one word. K's scale multiplies the score, V's the weight. Queries are brought into f16's range by a
-// power of two of each row (exact down to 2^-39 of the row's largest).
+// power of two of each row (all bits down to 2^-28 of the row's largest, to 2^-39 of it below).
 // f16 weights have 11 significant bits, where bf16 ones have 8, but 2^-24 is their least step, so V's scales must not
 // push them there: a unit's positions are taken in passes, each with those whose scale is within 2^kCaWindow of the
-// largest one left, E (one pass where the scales are alike, as a history's are); a weight is 2^(s - m - 8 + 15 + e - E), off by
-// at most 2^-24 of the largest weight where it is less than 2^-13 of it. A pass's sums are fp32 of their own, times 2^(E - 15) added
-// to the row's: what a row does not see, and rows of zeros (whose e is 0), can shift nothing out of it.
+// largest one left, E (one pass where the scales are alike, as a history's are; each further one costs as much again). A
+// weight is 2^(s - m - 8 + 15 + e - E), off by at most 2^-24 of the largest weight where it is less than 2^-13 of it. A
+// pass's sums are fp32 of their own, times 2^(E - 15) added to the row's: what a row does not see, and rows of zeros
+// (whose e is 0), can shift nothing out of it. Sums of a unit's own cost 3 % at 32 rows (171 us where one running E
+// took 167) and 1 % at one.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -70,7 +72,7 @@ constexpr int kCaTile = 32;     // positions of a unit
 // Warps of a CTA (one CTA per SM) for blocks of 16 mt rows. What is in flight is the same; the conversions of e4m3 fragments
 // leave gaps that more warps fill: 64 users, one row, d 512, histories of up to 15000 rows 121 us with 8 warps, 103 with
 // 12, 102 with 16. With 32 rows 12 warps have too few registers, and pairs of warps that share the tiles and
-// convert them twice take 178 us with 16 warps where 8 warps of 32 rows take 165.
+// convert them twice take 178 us with 16 warps where 8 warps of 32 rows took 165 (both before the passes by scale).
 constexpr int ca_warps(bool fp8, int mt) { return fp8 && mt == 1 ? 12 : 8; }
 constexpr int kCaMinUnits = 2;  // a warp's least share where there is little work: 12.1 us for one row of 8 heads over
                                 // 5000 positions; with 4 the units take longer, with 1 the join does (12.9, 13.3 us)

@@ -5,7 +5,7 @@
 // Bound: the exponentials. A tile of 128 rows x 128 positions takes 16384 of them, 1024 cycles of the SM's
 // special-function units (16 a cycle), beside 2 * 128 * 128 * d_head multiply-adds in 128 (d_head 32) or 256 cycles
 // each. (A share of them on the FMA pipe gained nothing: a softmax warp is as busy with the rest of a score.)
-// Four users' chunks of 1000 rows against histories of up to 15000 (8 heads, d 512): 117 us, 520 TFLOP/s; on e4m3 132 us.
+// Four users' chunks of 1000 rows against histories of up to 15000 (8 heads, d 512): 117 us, 520 TFLOP/s; on e4m3 130 us.
 //
 // One CTA per SM takes a contiguous slice of the units (128 positions of one item = (sequence, K|V head, block of 256
 // rows)), all items' units laid end to end; causal items end at their last row's position. Partials where a slice cuts an
@@ -29,7 +29,8 @@ constexpr int kCpUnit = 128;     // positions of a unit
 constexpr int cp_threads(bool fp8) { return fp8 ? 512 : 384; }
 constexpr int cp_producers(bool fp8) { return fp8 ? 4 : 2; }  // warps that write the tiles
 // Registers after the start: a row's 128 scores stay in a softmax thread's. With what the block was launched with
-// (65536 / threads, a multiple of 8) they must add up, or the last one would wait for ever.
+// (65536 / threads, a multiple of 8) they must add up, or the last one would wait for ever. The compiler allots the launch's
+// 168 (128) to all of them and spills 40 (24) bytes of a thread.
 constexpr int kCpRegsLoad = 88, kCpRegsSoftmax = 208;                               // bf16: 3 x 168
 constexpr int kCpRegsLoadE4m3 = 64, kCpRegsConvert = 96, kCpRegsSoftmaxE4m3 = 176;  // e4m3: 4 x 128
 static_assert(kCpRegsLoad + 2 * kCpRegsSoftmax <= 3 * 168 && kCpRegsLoadE4m3 + kCpRegsConvert + 2 * kCpRegsSoftmaxE4m3 <= 4 * 128,

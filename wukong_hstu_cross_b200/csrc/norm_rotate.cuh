@@ -14,7 +14,7 @@
 // warp's lanes cover 32 / LPH rows; a head's columns are one segment of 32 bytes or more, so loads and stores are whole
 // sectors. The next kNrHeads heads (the next row's first ones at a row's end) are loaded before the
 // present ones are used. Everything is held in fp32 and rounded once, at the store. Angles are reduced
-// in 64-bit fixed point: a position times the fraction of a turn that one position turns, modulo 1, keeps 2^-33 of
+// in 64-bit fixed point: a position times the fraction of a turn that one position turns, modulo 1, keeps 2^-31 of
 // a turn at any position, where fp32 would lose the angle of a far one.
 #pragma once
 

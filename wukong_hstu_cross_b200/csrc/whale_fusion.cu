@@ -2745,6 +2745,9 @@ whale_status plan_cache_attention(const Shape& s, const whale_cache& k, const wh
   // A batch whose average sequence is in the warp-level kernel's range while the longest is not: each kernel takes its
   // own, one after the other in the same workspace. 63 users with one new event and one with 200 (with 1000), d 512,
   // histories of up to 15000 rows: 178 us (198) where the tcgen05 kernel alone takes 318 (342); e4m3 136 (207) and 367 (405).
+  // The host knows the average alone, so a batch above the border goes to the tcgen05 kernel whatever its mix: 32 users
+  // with one row and 32 with 100 (an average of 50) take 302 us where sharing at 32 would take 246, 56 with one and 8 with 400 391
+  // and 246; uniform ones gain nothing from the two empty launches. 48 with one and 16 with 100 (26): 210.
   p->few = p->bm != kCpRows ? 0 : (all <= 16ll * c.B ? 16 : (all <= 32ll * c.B ? 32 : 0));
   // rows and positions are counted in 32 bits in the kernels
   if (c.total_new * s.h >= (1ll << 31) || c.max_length > (1 << 30)) return WHALE_ERR_UNSUPPORTED;
