@@ -19,10 +19,12 @@
 //
 // Products: warp-level m16n8k16 with fp32 sums. bf16 cache: K and V by ldmatrix; weights are rounded to bf16, V's
 // type, which both operands of a product have (one event's relative error is then 0.0023 where the rounding of the result
-// alone leaves 0.0016; the packed path rounds its weights the same way). e4m3 cache: the fragments are converted from the bytes in registers, to f16 (every e4m3 number is an f16 number); a lane's bytes of a K row are contiguous (the order of d_head inside a product is free as long as q has the same), and the
-// positions of a tile are numbered so that a lane's scores are 8 neighbouring ones, whose scales it
-// reads as one word. K's scale multiplies the score, V's the weight. Queries are brought into f16's range by a
-// power of two of each row (all bits down to 2^-28 of the row's largest, to 2^-39 of it below).
+// alone leaves 0.0016; the packed path rounds its weights the same way). e4m3 cache: the fragments are converted from the
+// bytes in registers, to f16 (every e4m3 number is an f16 number); a lane's bytes of a K row are contiguous (the order of
+// d_head inside a product is free as long as q has the same), and the positions of a tile are numbered so that a lane's
+// scores are 8 neighbouring ones, whose scales it reads as one word. K's scale multiplies the score, V's the weight.
+// Queries are brought into f16's range by a power of two of each row (all bits down to 2^-28 of the row's largest, to
+// 2^-39 of it below).
 // f16 weights have 11 significant bits, where bf16 ones have 8, but 2^-24 is their least step, so V's scales must not
 // push them there: a unit's positions are taken in passes, each with those whose scale is within 2^kCaWindow of the
 // largest one left, E (one pass where the scales are alike, as a history's are; each further one costs as much again). A

@@ -117,9 +117,10 @@ __global__ void __launch_bounds__(kRowsThreads, 5) cache_append_kernel(const Row
 
 // Read: the same lanes the other way; rows in no page come back as zeros. Each row's place is looked up by one
 // thread of the block (every load waits for it: 60 us where every lane looking up its own row took 69 us, 48
-// histories of 3000 to 6000 rows, d 256, e4m3).
+// histories of 3000 to 6000 rows, d 256, e4m3). bf16 rows take 101.2 us with registers
+// for 4 blocks an SM, 102.3 for 5 (24 histories, d 512); e4m3 rows need fewer and have 5.
 template <int DH, bool FP8>
-__global__ void __launch_bounds__(kRowsThreads) cache_read_kernel(const RowsArgs a) {
+__global__ void __launch_bounds__(kRowsThreads, FP8 ? 5 : 4) cache_read_kernel(const RowsArgs a) {
   constexpr int LPH = DH / 8, HU = kReadHeads, ROWS = rows_per_block(DH);
   __shared__ long long places[ROWS];
   pdl_wait();
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kRowsThreads) cache_read_kernel(const RowsArgs
         }
       }
     }
-    if constexpr (FP8) {  // behind all numbers: 60.6 us; each scale beside its head's numbers 69 us (the same histories)
+    if constexpr (FP8) {  // behind all numbers: 61 us; each scale beside its head's numbers 69 us (the same histories)
 #pragma unroll
       for (int k = 0; k < HU; ++k)
         if (at >= 0 && h0 + k < heads) sc[k] = a.scales[at + ((long long)(h0 + k) << a.c.page_shift)];
